@@ -73,7 +73,8 @@ extern "C" {
 #define MOE_ERR_WORKSPACE -4   /* ws_bytes smaller than moe_workspace_bytes()      */
 #define MOE_ERR_LAUNCH    -5   /* a kernel launch or HIP runtime call failed       */
 #define MOE_ERR_STATE     -6   /* no profiled forward yet; inconsistent host counts */
-#define MOE_ERR_ARG       -7   /* a setting outside its documented range           */
+#define MOE_ERR_ARG       -7   /* a setting outside its documented range, or a
+                                * pointer not aligned or not distinct as documented */
 
 #define MOE_F32   0
 #define MOE_BF16  1
@@ -433,6 +434,171 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
                      const int32_t* pos, const void* fwd_ws, size_t fwd_ws_bytes, void* dx, float* dlogits,
                      float* dw_gate, float* dw_up, float* dw_down, float* dw_router, void* ws, size_t ws_bytes,
                      void* stream);
+
+/* ---------------------------------------------------------------- the norm in front of the block
+ *
+ * Root-mean-square norm with the residual's addition, per token row:
+ *   s[t] = x[t] + residual[t],  rstd[t] = (mean_c s[t][c]^2 + eps)^(-1/2),
+ *   y[t][c] = s[t][c] rstd[t] weight[c]
+ * in float32; sum and y are rounded to nearest even where they are stored (y
+ * from the unrounded s).  For MOE_MXFP8 problems the rows' MXFP8 form can be
+ * written in the same pass: E4M3 codes and E8M0 scales of the stored bf16 y
+ * (MXFP8 as above, blocks of 32 along d), which moe_forward_quantized reads
+ * ("Section 24: Conclusion", 24.3: a quantiser should emit what the consumer
+ * reads without conversion; Evidence 6 counted separate quantise kernels as
+ * overhead).  Uses T, d_model and act_dtype of the problem.
+ *   x        : device [T, d] activation type (bf16 for MOE_MXFP8)
+ *   residual : device [T, d], or NULL: s = x
+ *   weight   : device [d], activation type
+ *   eps      : finite, >= 0
+ *   sum      : device [T, d] out, or NULL; may be x or residual (in place)
+ *   y        : device [T, d] out, may be x or residual (in place, if sum is
+ *              not the same); NULL only with yq
+ *   yq       : device uint8 [T, d] out, MOE_MXFP8 only, or NULL
+ *   yq_scale : device uint8 [T, d/32] out with yq, 4-byte aligned
+ *   rstd     : device float32 [T] out, or NULL (moe_norm_backward reads it)
+ * Tensors [T, d] and weight are 16-byte aligned, yq 8-byte aligned.
+ * Errors: MOE_ERR_NULL (x, weight, y and yq both, yq without yq_scale),
+ * MOE_ERR_DTYPE for yq on another act_dtype, MOE_ERR_ARG for eps, an
+ * unaligned pointer or y == sum. */
+int32_t moe_norm(const moe_problem* p, const void* x, const void* residual, const void* weight, float eps, void* sum,
+                 void* y, uint8_t* yq, uint8_t* yq_scale, float* rstd, void* stream);
+
+/* Gradients of moe_norm: with n = s rstd and u = dy weight,
+ *   ds[t] = rstd (u - n mean_c(u n)) + dsum[t],   dweight = sum_t dy n.
+ * ds is the gradient of x and of the residual alike.
+ *   dy      : device [T, d] activation type, the gradient of y
+ *   dsum    : device [T, d], the gradient of sum from its other consumers (the
+ *             residual stream), or NULL
+ *   s       : device [T, d], the forward's sum (x without a residual)
+ *   rstd    : device float32 [T] of the forward
+ *   ds      : device [T, d] out, may be dy or dsum (in place)
+ *   dweight : device float32 [d] out
+ *   ws      : device, moe_norm_backward_workspace_bytes (host-only query)
+ * Sums run in a fixed order (bitwise reproducible).  Tensors 16-byte aligned
+ * (rstd 4).  Errors: MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an
+ * unaligned pointer or ds == s. */
+int32_t moe_norm_backward_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_norm_backward(const moe_problem* p, const void* dy, const void* dsum, const void* s, const void* weight,
+                          const float* rstd, void* ds, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_forward of a MOE_MXFP8 block (d_model >= 256) whose token rows are
+ * already quantised: xq [T, d] codes and xq_scale [T, d/32] as moe_norm
+ * writes them (xq 16-byte, xq_scale 4-byte aligned).  No quantise pass runs;
+ * GEMM1 reads the given code rows.  x (bf16) is read by the learned router
+ * only and may be NULL with MOE_LOGITS_GIVEN.  Every output is bit for bit
+ * moe_forward's of the rows the codes were made from.  The codes are not
+ * copied to the workspace: a backward of this call is moe_backward_aux with
+ * the same xq.  Errors: as moe_forward, MOE_ERR_DTYPE for another act_dtype,
+ * MOE_ERR_SHAPE for d_model < 256, MOE_ERR_ARG for an unaligned pointer. */
+int32_t moe_forward_quantized(const moe_problem* p, const void* x, const uint8_t* xq, const uint8_t* xq_scale,
+                              const void* w_router, float* logits, const void* packed_w, void* y, int32_t* topk_idx,
+                              float* topk_gate, int32_t* counts, int32_t* offsets, int32_t* pos, float* router_stats,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- the router's losses
+ *
+ * Balance and z loss of the router with the per-expert counts (the report
+ * asks that requested counts be inspected next to the Switch-style scalar,
+ * "Section 24: Conclusion", 24.3 and Evidence 9 / Figure 45).  Over the N live
+ * tokens, p_t the softmax of logits[t], f_e = counts[e] / (N k):
+ *   loss[0] = E sum_e f_e P_e,  P_e = (1/N) sum_t p_te
+ *   loss[1] = (1/N) sum_t lse_t^2,  lse_t = log sum_e exp logits[t][e]
+ * moe_balance_loss_backward: with dloss = (g0, g1) and the counts constants,
+ *   dlogits[t][e] = (p_te / N) (g0 E (f_e - sum_j f_j p_tj) + 2 g1 lse_t),
+ * zero for tokens that are not live.  N = 0 gives zeros.  Uses T, n_experts
+ * and top_k of the problem.
+ *   logits : device float32 [T, E]; -inf excludes an expert from the softmax,
+ *            a live row of -inf alone counts as p = 0, lse = 0; rows that are
+ *            not live may hold anything
+ *   topk_idx : device int32 [T, k]; an index outside [0, E) is not counted
+ *   mask   : device uint8 [T], nonzero: the token is live; NULL: all are
+ *   counts : device int32 [E + 1]: out / in; counts[E] is N
+ *   loss   : device float32 [2] out
+ *   dloss  : device float32 [2], the gradient for the two losses
+ *   dlogits: device float32 [T, E] out
+ *   ws     : device, moe_balance_workspace_bytes (host-only query)
+ * Sums run in a fixed order (bitwise reproducible).  Errors: MOE_ERR_NULL,
+ * MOE_ERR_WORKSPACE. */
+int32_t moe_balance_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                         int32_t* counts, float* loss, void* ws, size_t ws_bytes, void* stream);
+int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, const uint8_t* mask,
+                                  const int32_t* counts, const float* dloss, float* dlogits, void* stream);
+
+/* Gradients of the router's product logits = x W_r from dense logit gradients:
+ *   dx[t] = dx_in[t] + sum_e dlogits[t][e] W_r[:, e],   dw_router = x^T dlogits
+ * accumulated in float32 (float32 operands enter the matrix cores as three
+ * bfloat16 terms each), dx rounded once.
+ *   dlogits  : device float32 [T, E]
+ *   x        : device [T, d] activation type (bf16 for MOE_MXFP8)
+ *   w_router : device [d, E], same type
+ *   dx_in    : device [T, d], same type, or NULL; dx may be dx_in (in place)
+ *   dx       : device [T, d] out;  dw_router : device float32 [d, E] out
+ *   ws       : device, moe_router_backward_workspace_bytes (host-only query;
+ *              may be 0: then ws may be NULL)
+ * Tensors are 16-byte aligned.  Sums run in a fixed order.  Errors:
+ * MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an unaligned pointer. */
+int32_t moe_router_backward_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const void* x, const void* w_router,
+                            const void* dx_in, void* dx, float* dw_router, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_backward with another gradient for the logits: dlogits_aux [T, E]
+ * float32 (moe_balance_loss_backward's), or NULL, is added to dlogits, and for
+ * the learned router dx and dw_router are the gradients of the router's
+ * product from that sum (dense, as moe_router_backward).  xq: the codes given
+ * to moe_forward_quantized when that was the forward, else NULL.  Other
+ * arguments as moe_backward; ws_bytes >= moe_backward_aux_workspace_bytes.
+ * With both NULL it is moe_backward.  Errors: as moe_backward; MOE_ERR_DTYPE /
+ * MOE_ERR_SHAPE for xq on a problem moe_forward_quantized does not take;
+ * MOE_ERR_ARG for an unaligned xq, or for dlogits_aux == dlogits. */
+int32_t moe_backward_aux_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, const void* w_router,
+                         const void* packed_w, const void* packed_bwd, const int32_t* topk_idx,
+                         const float* topk_gate, const int32_t* offsets, const int32_t* pos, const void* fwd_ws,
+                         size_t fwd_ws_bytes, void* dx, float* dlogits, float* dw_gate, float* dw_up, float* dw_down,
+                         float* dw_router, void* ws, size_t ws_bytes, void* stream, const float* dlogits_aux,
+                         const uint8_t* xq);
+
+/* ---------------------------------------------------------------- a few tokens (serving)
+ *
+ * The block for up to MOE_DECODE_MAX_TOKENS tokens with 4-bit expert weights:
+ * x, h, y bfloat16, weights MXFP4 (OCP Microscaling v1.0: E2M1 codes, one E8M0
+ * scale per 32 consecutive elements along the contraction axis, shared
+ * exponent floor(log2(amax)) - 2 clamped to [-127, 127], elements rounded to
+ * nearest even and saturated to +-6).  act_dtype MOE_BF16 or MOE_MXFP8 (no
+ * difference here), d_model and d_hidden multiples of 128, no
+ * MOE_IDENTITY_EXPERTS.
+ *
+ * moe_pack_weights_decode quantises w_gate, w_up [E, d, H], w_down [E, H, d]
+ * (device bfloat16) into packed, moe_decode_weight_bytes() bytes:
+ *   W1 codes [E][2H][d/2], row n of an expert as moe_pack_weights orders them;
+ *   W2 codes [E][d][H/2]; scales S1 [E][2H][d/32]; scales S2 [E][d][H/32];
+ * one after the other (every region is a multiple of 256 bytes), row-major,
+ * byte j of a code row holding element 2j in its low and 2j + 1 in its high
+ * four bits.  Weights already in that format can be given as they are.
+ *
+ * moe_decode_experts: y[t] = sum_j topk_gate[t][j] FFN_e(x[t]), e =
+ * topk_idx[t][j], summed in slot order in float32 and rounded once.  An index
+ * outside [0, E) is a slot not in use (a padded token's row of y is zero).
+ * moe_decode: router logits, top-k and gates as moe_route (bit for bit), then
+ * the experts; topk_idx and topk_gate may be NULL (kept in the workspace).
+ *   x [T, d] bf16; w_router [d, E] bf16 (NULL with MOE_LOGITS_GIVEN);
+ *   logits float32 [T, E]; topk_idx int32 [T, k]; topk_gate float32 [T, k];
+ *   y [T, d] bf16 out (not x); ws: moe_decode_workspace_bytes (host-only query)
+ * x, w_router, logits, packed, y and ws are 16-byte aligned.  Results do not depend on the other
+ * tokens of the call.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T over the limit,
+ * d or H not a multiple of 128), MOE_ERR_DTYPE, MOE_ERR_WORKSPACE,
+ * MOE_ERR_ARG for an unaligned pointer or y == x. */
+#define MOE_DECODE_MAX_TOKENS 256
+int32_t moe_decode_weight_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_decode_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_pack_weights_decode(const moe_problem* p, const void* w_gate, const void* w_up, const void* w_down,
+                                void* packed, void* stream);
+int32_t moe_decode_experts(const moe_problem* p, const void* x, const int32_t* topk_idx, const float* topk_gate,
+                           const void* packed, void* y, void* ws, size_t ws_bytes, void* stream);
+int32_t moe_decode(const moe_problem* p, const void* x, const void* w_router, float* logits, const void* packed,
+                   void* y, int32_t* topk_idx, float* topk_gate, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -27,7 +27,11 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_packe
            "moe_forward", "moe_forward_host_sync", "moe_set_profiling", "moe_kernel_times",
            "moe_set_gemm_grid_cap", "moe_backward_workspace_bytes", "moe_backward_weight_bytes",
            "moe_pack_weights_backward", "moe_backward", "moe_set_test_flags", "moe_route_noalloc",
-           "moe_fused_status"]
+           "moe_fused_status", "moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward",
+           "moe_forward_quantized", "moe_balance_workspace_bytes", "moe_balance_loss",
+           "moe_balance_loss_backward", "moe_router_backward_workspace_bytes", "moe_router_backward",
+           "moe_backward_aux_workspace_bytes", "moe_backward_aux", "moe_decode_weight_bytes",
+           "moe_decode_workspace_bytes", "moe_pack_weights_decode", "moe_decode_experts", "moe_decode"]
 
 
 class MoeError(RuntimeError):
@@ -90,6 +94,19 @@ def lib():
         L.moe_pack_weights_backward.argtypes = [PP, _P, _P, _P, _P, _P]
         L.moe_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P,
                                    _P, _SZ, _P]
+        for name in ("norm_backward_workspace", "balance_workspace", "router_backward_workspace",
+                     "backward_aux_workspace", "decode_weight", "decode_workspace"):
+            getattr(L, f"moe_{name}_bytes").argtypes = [PP, ctypes.POINTER(_SZ)]
+        L.moe_norm.argtypes = [PP, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P]
+        L.moe_norm_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_forward_quantized.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_balance_loss.argtypes = [PP, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_balance_loss_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P]
+        L.moe_router_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_backward_aux.argtypes = [*L.moe_backward.argtypes, _P, _P]
+        L.moe_pack_weights_decode.argtypes = [PP, _P, _P, _P, _P, _P]
+        L.moe_decode_experts.argtypes = [PP, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_decode.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_kernel_times.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float),
                                        _I32, ctypes.POINTER(_I32)]
         for name in EXPORTS:
@@ -136,6 +153,18 @@ def _expect(t, shape, dtype, name):
         raise ValueError(f"{name} is required")
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _bytes(fn: str, p: Problem) -> int:
+    n = _SZ()
+    _check(fn, getattr(lib(), fn)(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def _on_current(t, name="x"):
+    """The kernels run on the current device, on the given stream of it."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 # ----------------------------------------------------------------------------- host-only queries
@@ -302,9 +331,18 @@ class Forward:
         else:
             self.idx = self.gate = self.counts = self.offsets = self.pos = None
 
-    def __call__(self, x, packed=None, w_router=None, logits=None, stream=None):
+    def __call__(self, x, packed=None, w_router=None, logits=None, stream=None, xq=None, xq_scale=None):
+        """With xq [T, d] and xq_scale [T, d/32] (a Norm's q and q_scale) the block
+        runs on these MXFP8 rows (moe_forward_quantized); x is then read by the
+        learned router only, and may be None with given logits."""
         p = self.p
-        _expect(x, (p.T, p.d_model), storage_dtype(p.act), "x")
+        if xq is not None:
+            if self.host_sync:
+                raise ValueError("quantised rows and host_sync do not go together")
+            _expect(xq, (p.T, p.d_model), torch.uint8, "xq")
+            _expect(xq_scale, (p.T, p.d_model // 32), torch.uint8, "xq_scale")
+        if xq is None or x is not None or not p.flags & MOE_LOGITS_GIVEN:
+            _expect(x, (p.T, p.d_model), storage_dtype(p.act), "x")
         if p.flags & MOE_LOGITS_GIVEN:
             _expect(logits, (p.T, p.n_experts), torch.float32, "logits")
             if logits.data_ptr() != self.logits.data_ptr():
@@ -314,7 +352,10 @@ class Forward:
         args = (ctypes.byref(p), _ptr(x), _ptr(w_router), _ptr(self.logits), _ptr(packed), _ptr(self.y),
                 _ptr(self.idx), _ptr(self.gate), _ptr(self.counts), _ptr(self.offsets), _ptr(self.pos),
                 _ptr(self.router_stats), _ptr(self.ws), self.ws.numel(), _stream(stream))
-        if self.host_sync:
+        if xq is not None:
+            _check("moe_forward_quantized", lib().moe_forward_quantized(
+                args[0], args[1], _ptr(xq), _ptr(xq_scale), *args[2:]))
+        elif self.host_sync:
             _check("moe_forward_host_sync", lib().moe_forward_host_sync(
                 *args, ctypes.c_void_p(self.host_counts.data_ptr())))
         else:
@@ -360,12 +401,14 @@ def pack_weights_backward(p: Problem, w_gate, w_up, w_down, stream=None) -> torc
 
 
 class Backward:
-    """Preallocated gradients and workspace for moe_backward of a Forward's last call."""
+    """Preallocated gradients and workspace for moe_backward of a Forward's last call
+    (aux: for moe_backward_aux with another gradient for the logits)."""
 
-    def __init__(self, p: Problem, device):
+    def __init__(self, p: Problem, device, aux: bool = False):
         self.p = p
         T, E, d, H = p.T, p.n_experts, p.d_model, p.d_hidden
-        self.ws = torch.empty(backward_workspace_bytes(p), dtype=torch.uint8, device=device)
+        self.ws = torch.empty(_bytes("moe_backward_aux_workspace_bytes", p) if aux else backward_workspace_bytes(p),
+                              dtype=torch.uint8, device=device)
         self.dx = torch.empty((T, d), dtype=out_dtype(p.act), device=device)
         self.dlogits = torch.empty((T, E), dtype=torch.float32, device=device)
         self.dw_gate = torch.empty((E, d, H), dtype=torch.float32, device=device)
@@ -374,22 +417,219 @@ class Backward:
         self.dw_router = (None if p.flags & MOE_LOGITS_GIVEN
                           else torch.empty((d, E), dtype=torch.float32, device=device))
 
-    def __call__(self, fwd: "Forward", dy, packed, packed_bwd, x=None, w_router=None, stream=None):
+    def __call__(self, fwd: "Forward", dy, packed, packed_bwd, x=None, w_router=None, stream=None,
+                 dlogits_aux=None, xq=None):
+        """dlogits_aux [T, E]: a gradient for the logits to be added (BalanceLoss.backward's);
+        xq: the codes the forward was given, if it was given any."""
         p = self.p
         dt = storage_dtype(p.act)
+        if dlogits_aux is not None:
+            _expect(dlogits_aux, (p.T, p.n_experts), torch.float32, "dlogits_aux")
+        if xq is not None:
+            _expect(xq, (p.T, p.d_model), torch.uint8, "xq")
         _expect(dy, (p.T, p.d_model), dt, "dy")
         if not p.flags & MOE_LOGITS_GIVEN:
             _expect(x, (p.T, p.d_model), dt, "x")
             _expect(w_router, (p.d_model, p.n_experts), dt, "w_router")
         elif x is not None:
             _expect(x, (p.T, p.d_model), dt, "x")
-        _check("moe_backward", lib().moe_backward(
-            ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(w_router), _ptr(packed), _ptr(packed_bwd),
-            _ptr(fwd.idx), _ptr(fwd.gate), _ptr(fwd.offsets), _ptr(fwd.pos), _ptr(fwd.ws), fwd.ws.numel(),
-            _ptr(self.dx), _ptr(self.dlogits), _ptr(self.dw_gate), _ptr(self.dw_up), _ptr(self.dw_down),
-            _ptr(self.dw_router), _ptr(self.ws), self.ws.numel(), _stream(stream)))
+        args = (ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(w_router), _ptr(packed), _ptr(packed_bwd),
+                _ptr(fwd.idx), _ptr(fwd.gate), _ptr(fwd.offsets), _ptr(fwd.pos), _ptr(fwd.ws), fwd.ws.numel(),
+                _ptr(self.dx), _ptr(self.dlogits), _ptr(self.dw_gate), _ptr(self.dw_up), _ptr(self.dw_down),
+                _ptr(self.dw_router), _ptr(self.ws), self.ws.numel(), _stream(stream))
+        if dlogits_aux is None and xq is None:
+            _check("moe_backward", lib().moe_backward(*args))
+        else:
+            _check("moe_backward_aux", lib().moe_backward_aux(*args, _ptr(dlogits_aux), _ptr(xq)))
         return dict(dx=self.dx, dlogits=self.dlogits, dw_gate=self.dw_gate, dw_up=self.dw_up,
                     dw_down=self.dw_down, dw_router=self.dw_router)
+
+
+class Norm:
+    """Preallocated outputs of moe_norm: y [T, d], rstd [T], with a residual its
+    sum [T, d], for MXFP8 problems the rows' codes q [T, d] and scales q_scale
+    [T, d/32] (uint8) unless quantized is False."""
+
+    def __init__(self, p: Problem, device, eps: float = 1e-6, residual: bool = True, quantized: bool | None = None):
+        self.p, self.eps = p, float(eps)
+        T, d, dt = p.T, p.d_model, storage_dtype(p.act)
+        if quantized is None:
+            quantized = p.act == "mxfp8"
+        self.y = torch.empty((T, d), dtype=dt, device=device)
+        self.sum = torch.empty((T, d), dtype=dt, device=device) if residual else None
+        self.rstd = torch.empty((T,), dtype=torch.float32, device=device)
+        self.q = torch.empty((T, d), dtype=torch.uint8, device=device) if quantized else None
+        self.q_scale = torch.empty((T, d // 32), dtype=torch.uint8, device=device) if quantized else None
+
+    def __call__(self, x, weight, residual=None, stream=None):
+        """y = norm(x + residual) weight; returns y."""
+        p = self.p
+        dt = storage_dtype(p.act)
+        _expect(x, (p.T, p.d_model), dt, "x")
+        _expect(weight, (p.d_model,), dt, "weight")
+        if (residual is None) != (self.sum is None):
+            raise ValueError("residual: " + ("expected" if residual is None else "not expected"))
+        if residual is not None:
+            _expect(residual, (p.T, p.d_model), dt, "residual")
+        _on_current(x)
+        _check("moe_norm", lib().moe_norm(
+            ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(weight), self.eps, _ptr(self.sum), _ptr(self.y),
+            _ptr(self.q), _ptr(self.q_scale), _ptr(self.rstd), _stream(stream)))
+        return self.y
+
+
+class NormBackward:
+    """Preallocated gradients and workspace of moe_norm_backward."""
+
+    def __init__(self, p: Problem, device):
+        self.p = p
+        self.ws = torch.empty(_bytes("moe_norm_backward_workspace_bytes", p), dtype=torch.uint8, device=device)
+        self.ds = torch.empty((p.T, p.d_model), dtype=storage_dtype(p.act), device=device)
+        self.dweight = torch.empty((p.d_model,), dtype=torch.float32, device=device)
+
+    def __call__(self, dy, s, weight, rstd, dsum=None, stream=None) -> dict:
+        """dy: the gradient of y; s: the forward's sum (x without a residual); dsum: the
+        gradient of that sum from elsewhere.  dict(ds, dweight)."""
+        p = self.p
+        dt = storage_dtype(p.act)
+        _expect(dy, (p.T, p.d_model), dt, "dy")
+        _expect(s, (p.T, p.d_model), dt, "s")
+        _expect(weight, (p.d_model,), dt, "weight")
+        _expect(rstd, (p.T,), torch.float32, "rstd")
+        if dsum is not None:
+            _expect(dsum, (p.T, p.d_model), dt, "dsum")
+        _on_current(dy, "dy")
+        _check("moe_norm_backward", lib().moe_norm_backward(
+            ctypes.byref(p), _ptr(dy), _ptr(dsum), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(self.ds),
+            _ptr(self.dweight), _ptr(self.ws), self.ws.numel(), _stream(stream)))
+        return dict(ds=self.ds, dweight=self.dweight)
+
+
+class BalanceLoss:
+    """Preallocated outputs and workspace of moe_balance_loss and its backward:
+    loss [2] (balance, z), counts [E], live [1] (tokens), dlogits [T, E]."""
+
+    def __init__(self, p: Problem, device):
+        self.p = p
+        self.ws = torch.empty(_bytes("moe_balance_workspace_bytes", p), dtype=torch.uint8, device=device)
+        self.loss = torch.empty((2,), dtype=torch.float32, device=device)
+        self.counts_live = torch.empty((p.n_experts + 1,), dtype=torch.int32, device=device)
+        self.counts, self.live = self.counts_live[:-1], self.counts_live[-1:]
+        self.dlogits = torch.empty((p.T, p.n_experts), dtype=torch.float32, device=device)
+
+    def _expect_logits(self, logits, mask):
+        p = self.p
+        _expect(logits, (p.T, p.n_experts), torch.float32, "logits")
+        if mask is not None:
+            _expect(mask, (p.T,), torch.uint8, "mask")
+        _on_current(logits, "logits")
+
+    def __call__(self, logits, idx, mask=None, stream=None):
+        """loss [2] of the tokens whose mask (uint8 [T]; None: all) is not zero."""
+        p = self.p
+        self._expect_logits(logits, mask)
+        _expect(idx, (p.T, p.top_k), torch.int32, "idx")
+        _check("moe_balance_loss", lib().moe_balance_loss(
+            ctypes.byref(p), _ptr(logits), _ptr(idx), _ptr(mask), _ptr(self.counts_live), _ptr(self.loss),
+            _ptr(self.ws), self.ws.numel(), _stream(stream)))
+        return self.loss
+
+    def backward(self, logits, dloss, mask=None, stream=None):
+        """dlogits for dloss [2], with the counts of the last call."""
+        self._expect_logits(logits, mask)
+        _expect(dloss, (2,), torch.float32, "dloss")
+        _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+            ctypes.byref(self.p), _ptr(logits), _ptr(mask), _ptr(self.counts_live), _ptr(dloss), _ptr(self.dlogits),
+            _stream(stream)))
+        return self.dlogits
+
+
+class RouterBackward:
+    """Preallocated gradients and workspace of moe_router_backward."""
+
+    def __init__(self, p: Problem, device):
+        self.p = p
+        self.ws = torch.empty(_bytes("moe_router_backward_workspace_bytes", p), dtype=torch.uint8, device=device)
+        self.dx = torch.empty((p.T, p.d_model), dtype=storage_dtype(p.act), device=device)
+        self.dw_router = torch.empty((p.d_model, p.n_experts), dtype=torch.float32, device=device)
+
+    def __call__(self, dlogits, x, w_router, dx_in=None, stream=None) -> dict:
+        p = self.p
+        dt = storage_dtype(p.act)
+        _expect(dlogits, (p.T, p.n_experts), torch.float32, "dlogits")
+        _expect(x, (p.T, p.d_model), dt, "x")
+        _expect(w_router, (p.d_model, p.n_experts), dt, "w_router")
+        if dx_in is not None:
+            _expect(dx_in, (p.T, p.d_model), dt, "dx_in")
+        _on_current(x)
+        _check("moe_router_backward", lib().moe_router_backward(
+            ctypes.byref(p), _ptr(dlogits), _ptr(x), _ptr(w_router), _ptr(dx_in), _ptr(self.dx), _ptr(self.dw_router),
+            _ptr(self.ws) if self.ws.numel() else None, self.ws.numel(), _stream(stream)))
+        return dict(dx=self.dx, dw_router=self.dw_router)
+
+
+MOE_DECODE_MAX_TOKENS = 256
+
+
+def decode_weight_bytes(p: Problem) -> int:
+    return _bytes("moe_decode_weight_bytes", p)
+
+
+def pack_weights_decode(p: Problem, w_gate, w_up, w_down, stream=None) -> torch.Tensor:
+    """The MXFP4 weights of moe_decode from bfloat16 ones."""
+    E, d, H = p.n_experts, p.d_model, p.d_hidden
+    _expect(w_gate, (E, d, H), torch.bfloat16, "w_gate")
+    _expect(w_up, (E, d, H), torch.bfloat16, "w_up")
+    _expect(w_down, (E, H, d), torch.bfloat16, "w_down")
+    _on_current(w_gate, "w_gate")
+    packed = torch.empty(decode_weight_bytes(p), dtype=torch.uint8, device=w_gate.device)
+    _check("moe_pack_weights_decode", lib().moe_pack_weights_decode(
+        ctypes.byref(p), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(packed), _stream(stream)))
+    return packed
+
+
+class Decode:
+    """Preallocated output and workspace of the block for a few tokens with 4-bit
+    weights (moe_decode, moe_decode_experts): y [T, d], logits [T, E], idx and
+    gate [T, k]."""
+
+    def __init__(self, p: Problem, device):
+        self.p = p
+        self.weight_bytes = decode_weight_bytes(p)
+        self.ws = torch.empty(_bytes("moe_decode_workspace_bytes", p), dtype=torch.uint8, device=device)
+        self.y = torch.empty((p.T, p.d_model), dtype=torch.bfloat16, device=device)
+        self.logits = torch.empty((p.T, p.n_experts), dtype=torch.float32, device=device)
+        self.idx = torch.empty((p.T, p.top_k), dtype=torch.int32, device=device)
+        self.gate = torch.empty((p.T, p.top_k), dtype=torch.float32, device=device)
+
+    def __call__(self, x, packed, w_router=None, logits=None, stream=None):
+        """The block: router logits (or given ones), top-k and gates, experts; returns y."""
+        p = self.p
+        _expect(x, (p.T, p.d_model), torch.bfloat16, "x")
+        _expect(packed, (self.weight_bytes,), torch.uint8, "packed")
+        if p.flags & MOE_LOGITS_GIVEN:
+            _expect(logits, (p.T, p.n_experts), torch.float32, "logits")
+        else:
+            _expect(w_router, (p.d_model, p.n_experts), torch.bfloat16, "w_router")
+            logits = self.logits
+        _on_current(x)
+        _check("moe_decode", lib().moe_decode(
+            ctypes.byref(p), _ptr(x), _ptr(w_router), _ptr(logits), _ptr(packed), _ptr(self.y), _ptr(self.idx),
+            _ptr(self.gate), _ptr(self.ws), self.ws.numel(), _stream(stream)))
+        return self.y
+
+    def experts(self, x, idx, gate, packed, stream=None):
+        """The experts idx [T, k] (outside [0, E): unused) of each token, weighted by gate; returns y."""
+        p = self.p
+        _expect(x, (p.T, p.d_model), torch.bfloat16, "x")
+        _expect(idx, (p.T, p.top_k), torch.int32, "idx")
+        _expect(gate, (p.T, p.top_k), torch.float32, "gate")
+        _expect(packed, (self.weight_bytes,), torch.uint8, "packed")
+        _on_current(x)
+        _check("moe_decode_experts", lib().moe_decode_experts(
+            ctypes.byref(p), _ptr(x), _ptr(idx), _ptr(gate), _ptr(packed), _ptr(self.y), _ptr(self.ws),
+            self.ws.numel(), _stream(stream)))
+        return self.y
 
 
 def set_gemm_grid_cap(cap: int):

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
-SOURCES = ["route.hip", "dispatch.hip", "gemm.hip", "gemm_pipe.hip", "pack.hip", "backward.hip", "api.cpp"]
+SOURCES = ["route.hip", "dispatch.hip", "gemm.hip", "gemm_pipe.hip", "pack.hip", "backward.hip", "norm.hip",
+           "balance.hip", "router_bwd.hip", "decode.hip", "api.cpp"]
 ARCH = "gfx950"
 
 

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -187,9 +188,73 @@ int32_t check_problem(const moe_problem* p) {
     return MOE_OK;
 }
 
+// Problems whose forward can take quantised token rows.
+int32_t check_quantized(const moe_problem* p) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (p->act_dtype != MOE_MXFP8) return MOE_ERR_DTYPE;
+    return forward_quantises_tokens(*p) ? MOE_OK : MOE_ERR_SHAPE;
+}
+
 int32_t launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
 char* at(void* base, size_t off) { return static_cast<char*>(base) + off; }
+
+// Whether a pointer given (NULL is not) is off its alignment.
+bool off_by(const void* ptr, size_t align) { return (reinterpret_cast<uintptr_t>(ptr) & (align - 1)) != 0; }
+
+// moe_backward_aux: the backward's workspace, then the partial sums of the
+// dense router weight gradient.
+size_t bwd_aux_bytes(const moe_problem& p) {
+    const bool learned = !(p.flags & MOE_LOGITS_GIVEN);
+    return bwd_layout(p).total + (learned ? align256(router_dw_part_bytes(p.T, p.d_model, p.n_experts)) : 0);
+}
+
+// Balance loss: float sums [blocks][E] and [blocks], then int counts likewise.
+size_t balance_part_bytes(const moe_problem& p) {
+    return align256((size_t)balance_blocks(p.T, p.n_experts) * (p.n_experts + 1) * 4);
+}
+
+// Problems of the 4-bit decode form.
+int32_t check_decode(const moe_problem* p) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (p->act_dtype == MOE_F32 || (p->flags & MOE_IDENTITY_EXPERTS)) return MOE_ERR_DTYPE;
+    if (p->T > MOE_DECODE_MAX_TOKENS || p->d_model % 128 || p->d_hidden % 128) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+static_assert(kDecodeTokens == MOE_DECODE_MAX_TOKENS && kDecodeTokens <= kRouteBlock, "one routing block");
+
+// MXFP4 weights: every region is a multiple of 256 bytes.
+Packed decode_packed(const moe_problem& p) {
+    Packed P{};
+    const size_t E = p.n_experts, d = p.d_model, H = p.d_hidden;
+    P.w1 = 0;
+    P.w2 = E * 2 * H * d / 2;
+    P.s1 = P.w2 + E * d * H / 2;
+    P.s2 = P.s1 + E * 2 * H * d / 32;
+    P.total = P.s2 + E * d * H / 32;
+    return P;
+}
+
+struct DecodeLayout {
+    size_t h, ye, idx, gate, sel, rwt, total;
+};
+
+DecodeLayout decode_layout(const moe_problem& p) {
+    DecodeLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) { size_t o = off; off += align256(bytes); return o; };
+    const size_t R = (size_t)p.T * p.top_k, E = p.n_experts, d = p.d_model;
+    L.h = take(R * p.d_hidden * 2);
+    L.ye = take(R * d * 4);
+    L.idx = take(R * 4);
+    L.gate = take(R * 4);
+    L.sel = take((R + E) * 4);   // launch_route_select's scratch
+    L.rwt = take(!(p.flags & MOE_LOGITS_GIVEN) && E % 8 ? E * d * 2 : 0);   // router W^T
+    L.total = off;
+    return L;
+}
 
 // ------------------------------------------------------------------ profiling (moe_forward only)
 // Events are recorded on the forward's own stream before the first kernel and
@@ -255,7 +320,7 @@ const char* moe_status_string(int32_t status) {
         case MOE_ERR_WORKSPACE: return "workspace too small";
         case MOE_ERR_LAUNCH: return "kernel launch or HIP runtime call failed";
         case MOE_ERR_STATE: return "no profiled forward, or inconsistent host counts";
-        case MOE_ERR_ARG: return "setting out of range";
+        case MOE_ERR_ARG: return "setting out of range, or pointer not aligned or not distinct";
         default: return "unknown status";
     }
 }
@@ -448,12 +513,13 @@ namespace {
 int32_t forward_impl(const moe_problem* p, const void* x, const void* w_router, float* logits,
                      const void* packed_w, void* y, int32_t* topk_idx, float* topk_gate,
                      int32_t* counts, int32_t* offsets, int32_t* pos, float* router_stats, void* ws,
-                     size_t ws_bytes, void* stream, int32_t* host_counts) {
+                     size_t ws_bytes, void* stream, int32_t* host_counts, const uint8_t* xq = nullptr,
+                     const uint8_t* xq_scale = nullptr) {
     int32_t st = check_problem(p);
     if (st) return st;
     const bool given = p->flags & MOE_LOGITS_GIVEN;
     const bool identity = p->flags & MOE_IDENTITY_EXPERTS;
-    if (!x || !logits || !y || !ws || (!identity && !packed_w)) return MOE_ERR_NULL;
+    if ((!x && !(xq && given)) || !logits || !y || !ws || (!identity && !packed_w)) return MOE_ERR_NULL;
     if (!given && !w_router) return MOE_ERR_NULL;
     const Layout L = layout(*p);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
@@ -503,6 +569,13 @@ int32_t forward_impl(const moe_problem* p, const void* x, const void* w_router, 
         // through row_token, so only the positions are finalised here
         if ((st = launched(launch_route_finalize(idx, base, T, E, k, ps, row_token, s)))) return st;
         if ((st = prof_mark("route_finalize", s))) return st;
+    } else if (xq) {
+        // the caller's code rows: only the positions and the scales' layout are left to do
+        if ((st = launched(launch_route_finalize(idx, base, T, E, k, ps, row_token, s)))) return st;
+        if ((st = prof_mark("route_finalize", s))) return st;
+        if ((st = launched(launch_scale_gather(reinterpret_cast<const uint32_t*>(xq_scale), row_token, xs, R, d, s))))
+            return st;
+        if ((st = prof_mark("scale_gather", s))) return st;
     } else if (forward_quantises_tokens(*p)) {
         // each token quantised once (positions finalised in the same pass);
         // GEMM1 reads its code rows through row_token, and only the scales are
@@ -533,7 +606,7 @@ int32_t forward_impl(const moe_problem* p, const void* x, const void* w_router, 
             if ((st = prof_mark("grouped_ffn", s))) return st;
         } else {
             uint16_t* ab = keeps_gate_up(*p) ? reinterpret_cast<uint16_t*>(at(ws, L.ab)) : nullptr;
-            if ((st = launched(launch_gemm1(act, xe, xs, pw + P.w1, reinterpret_cast<const uint8_t*>(pw + P.s1),
+            if ((st = launched(launch_gemm1(act, xq ? xq : xe, xs, pw + P.w1, reinterpret_cast<const uint8_t*>(pw + P.s1),
                                             off, h, hs, R, E, d, H, host_counts, s,
                                             forward_quantises_tokens(*p) ? row_token : nullptr, ab))))
                 return st;
@@ -569,6 +642,18 @@ int32_t moe_forward_host_sync(const moe_problem* p, const void* x, const void* w
     if (!host_counts) return MOE_ERR_NULL;
     return forward_impl(p, x, w_router, logits, packed_w, y, topk_idx, topk_gate, counts, offsets, pos,
                         router_stats, ws, ws_bytes, stream, host_counts);
+}
+
+int32_t moe_forward_quantized(const moe_problem* p, const void* x, const uint8_t* xq, const uint8_t* xq_scale,
+                              const void* w_router, float* logits, const void* packed_w, void* y, int32_t* topk_idx,
+                              float* topk_gate, int32_t* counts, int32_t* offsets, int32_t* pos, float* router_stats,
+                              void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_quantized(p);
+    if (st) return st;
+    if (!xq || !xq_scale) return MOE_ERR_NULL;
+    if (off_by(xq, 16) || off_by(xq_scale, 4)) return MOE_ERR_ARG;
+    return forward_impl(p, x, w_router, logits, packed_w, y, topk_idx, topk_gate, counts, offsets, pos, router_stats,
+                        ws, ws_bytes, stream, nullptr, xq, xq_scale);
 }
 
 int32_t moe_set_profiling(int32_t enable) {
@@ -688,11 +773,15 @@ int32_t moe_pack_weights_backward(const moe_problem* p, const void* w_gate, cons
     return launched(launch_copy_bytes(w_down, at(packed_bwd, P.wd), (size_t)E * H * d * act_bytes(p->act_dtype), s));
 }
 
-int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const void* w_router, const void* packed_w,
-                     const void* packed_bwd, const int32_t* topk_idx, const float* topk_gate, const int32_t* offsets,
-                     const int32_t* pos, const void* fwd_ws, size_t fwd_ws_bytes, void* dx, float* dlogits,
-                     float* dw_gate, float* dw_up, float* dw_down, float* dw_router, void* ws, size_t ws_bytes,
-                     void* stream) {
+// The backward; aux (optional) is added to dlogits, and with it the learned
+// router's product is differentiated densely, its partial sums `part` behind
+// the workspace; xq (optional): the code rows of a moe_forward_quantized.
+static int32_t backward_impl(const moe_problem* p, const void* dy, const void* x, const void* w_router,
+                             const void* packed_w, const void* packed_bwd, const int32_t* topk_idx,
+                             const float* topk_gate, const int32_t* offsets, const int32_t* pos, const void* fwd_ws,
+                             size_t fwd_ws_bytes, void* dx, float* dlogits, float* dw_gate, float* dw_up,
+                             float* dw_down, float* dw_router, void* ws, size_t ws_bytes, void* stream,
+                             const float* aux, const uint8_t* xq) {
     int32_t st = check_backward(p);
     if (st) return st;
     const bool given = p->flags & MOE_LOGITS_GIVEN;
@@ -705,7 +794,7 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
     if (regather && !x) return MOE_ERR_NULL;
     const Layout L = layout(*p);
     const BwdLayout BL = bwd_layout(*p);
-    if (fwd_ws_bytes < L.total || ws_bytes < BL.total) return MOE_ERR_WORKSPACE;
+    if (fwd_ws_bytes < L.total || ws_bytes < (aux ? bwd_aux_bytes(*p) : BL.total)) return MOE_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int T = p->T, E = p->n_experts, k = p->top_k, d = p->d_model, H = p->d_hidden;
     const int R = T * k, act = bwd_act(p->act_dtype);
@@ -728,7 +817,7 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
         // the forward kept one code row per token when it quantised tokens: gathered through row_token
         const int32_t* rows = forward_quantises_tokens(*p) ? reinterpret_cast<const int32_t*>(at(fw, L.row_token))
                                                            : nullptr;
-        if ((st = launched(launch_dq_mxfp8(static_cast<const uint8_t*>(xe),
+        if ((st = launched(launch_dq_mxfp8(xq ? xq : static_cast<const uint8_t*>(xe),
                                            reinterpret_cast<const uint8_t*>(at(fw, L.xe_scale)), R, d, xe16, s,
                                            rows))))
             return st;
@@ -750,7 +839,8 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
     float* dsel = reinterpret_cast<float*>(at(ws, BL.dsel));
 
     float* srow = given ? nullptr : reinterpret_cast<float*>(at(ws, BL.srow));
-    if ((st = launched(launch_combine_bwd(act, dy, ye, gate, ps, idx, dye, dlogits, dsel, srow, T, d, E, k, s))))
+    if ((st = launched(launch_combine_bwd(act, dy, ye, gate, ps, idx, dye, dlogits, dsel, srow, T, d, E, k, s,
+                                        aux))))
         return st;
     const bool bf = act == MOE_BF16;
     const bool chain = use_bwd_chain(*p);
@@ -800,6 +890,11 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
     }
     if (!(bf && chain) && (st = launched(launch_gemm_plain(act, ab, pb + BP.w1t, dye, off, R, E, d, 2 * H, d, s))))
         return st;
+    if (aux && !given) {   // dL is dense: dx = sum_j dxe + dL W_r^T and dW_r = x^T dL, each rounded once
+        if ((st = launched(launch_router_dx(act, dlogits, w_router, dye, ps, k, dx, T, d, E, s)))) return st;
+        return launched(launch_router_dw(act, dlogits, x, reinterpret_cast<float*>(at(ws, BL.total)), dw_router, T, d,
+                                         E, s));
+    }
     void* wrt = given ? nullptr : at(ws, BL.wrt);
     if (!given && (st = launched(launch_router_transpose(act, w_router, d, E, wrt, s)))) return st;
     if ((st = launched(launch_dx(act, dye, ps, idx, dsel, wrt, dx, T, d, E, k, s)))) return st;
@@ -808,6 +903,206 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
                                                       reinterpret_cast<float*>(at(ws, BL.rpart)), dw_router, s))))
         return st;
     return MOE_OK;
+}
+
+int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const void* w_router, const void* packed_w,
+                     const void* packed_bwd, const int32_t* topk_idx, const float* topk_gate, const int32_t* offsets,
+                     const int32_t* pos, const void* fwd_ws, size_t fwd_ws_bytes, void* dx, float* dlogits,
+                     float* dw_gate, float* dw_up, float* dw_down, float* dw_router, void* ws, size_t ws_bytes,
+                     void* stream) {
+    return backward_impl(p, dy, x, w_router, packed_w, packed_bwd, topk_idx, topk_gate, offsets, pos, fwd_ws,
+                         fwd_ws_bytes, dx, dlogits, dw_gate, dw_up, dw_down, dw_router, ws, ws_bytes, stream, nullptr,
+                         nullptr);
+}
+
+int32_t moe_backward_aux_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_backward(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = bwd_aux_bytes(*p);
+    return MOE_OK;
+}
+
+int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, const void* w_router,
+                         const void* packed_w, const void* packed_bwd, const int32_t* topk_idx,
+                         const float* topk_gate, const int32_t* offsets, const int32_t* pos, const void* fwd_ws,
+                         size_t fwd_ws_bytes, void* dx, float* dlogits, float* dw_gate, float* dw_up, float* dw_down,
+                         float* dw_router, void* ws, size_t ws_bytes, void* stream, const float* dlogits_aux,
+                         const uint8_t* xq) {
+    int32_t st = MOE_OK;
+    if (xq && (st = check_quantized(p))) return st;
+    if (off_by(xq, 16) || (dlogits_aux && dlogits_aux == dlogits)) return MOE_ERR_ARG;
+    return backward_impl(p, dy, x, w_router, packed_w, packed_bwd, topk_idx, topk_gate, offsets, pos, fwd_ws,
+                         fwd_ws_bytes, dx, dlogits, dw_gate, dw_up, dw_down, dw_router, ws, ws_bytes, stream,
+                         dlogits_aux, xq);
+}
+
+// ----------------------------------------------------------------------------- norm
+
+int32_t moe_norm(const moe_problem* p, const void* x, const void* residual, const void* weight, float eps, void* sum,
+                 void* y, uint8_t* yq, uint8_t* yq_scale, float* rstd, void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (yq && p->act_dtype != MOE_MXFP8) return MOE_ERR_DTYPE;
+    if (!x || !weight || (!y && !yq) || (yq && !yq_scale)) return MOE_ERR_NULL;
+    if (!std::isfinite(eps) || eps < 0.f || off_by(x, 16) || off_by(residual, 16) || off_by(weight, 16) ||
+        off_by(sum, 16) || off_by(y, 16) || off_by(yq, 8) || (yq && off_by(yq_scale, 4)) || off_by(rstd, 4) ||
+        (y && y == sum))
+        return MOE_ERR_ARG;
+    return launched(launch_norm(p->act_dtype, x, residual, weight, eps, sum, y, yq, yq_scale, rstd, p->T, p->d_model,
+                                static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_norm_backward_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = align256(norm_bwd_part_bytes(p->act_dtype, p->T, p->d_model));
+    return MOE_OK;
+}
+
+int32_t moe_norm_backward(const moe_problem* p, const void* dy, const void* dsum, const void* s, const void* weight,
+                          const float* rstd, void* ds, float* dweight, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!dy || !s || !weight || !rstd || !ds || !dweight || !ws) return MOE_ERR_NULL;
+    if (off_by(dy, 16) || off_by(dsum, 16) || off_by(s, 16) || off_by(weight, 16) || off_by(rstd, 4) ||
+        off_by(ds, 16) || off_by(dweight, 16) || off_by(ws, 16) || ds == s)
+        return MOE_ERR_ARG;
+    if (ws_bytes < align256(norm_bwd_part_bytes(p->act_dtype, p->T, p->d_model))) return MOE_ERR_WORKSPACE;
+    return launched(launch_norm_bwd(p->act_dtype, dy, dsum, s, weight, rstd, ds, dweight, static_cast<float*>(ws),
+                                    p->T, p->d_model, static_cast<hipStream_t>(stream)));
+}
+
+// ----------------------------------------------------------------------------- router losses
+
+int32_t moe_balance_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = balance_part_bytes(*p) * 2;
+    return MOE_OK;
+}
+
+int32_t moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                         int32_t* counts, float* loss, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!logits || !topk_idx || !counts || !loss || !ws) return MOE_ERR_NULL;
+    const size_t part = balance_part_bytes(*p);
+    if (ws_bytes < 2 * part) return MOE_ERR_WORKSPACE;
+    return launched(launch_balance(logits, topk_idx, mask, p->T, p->n_experts, p->top_k, counts, loss,
+                                   static_cast<float*>(ws), reinterpret_cast<int32_t*>(at(ws, part)),
+                                   static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, const uint8_t* mask,
+                                  const int32_t* counts, const float* dloss, float* dlogits, void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!logits || !counts || !dloss || !dlogits) return MOE_ERR_NULL;
+    return launched(launch_balance_bwd(logits, mask, counts, dloss, p->T, p->n_experts, p->top_k, dlogits,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_router_backward_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = align256(router_dw_part_bytes(p->T, p->d_model, p->n_experts));
+    return MOE_OK;
+}
+
+int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const void* x, const void* w_router,
+                            const void* dx_in, void* dx, float* dw_router, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    const size_t need = align256(router_dw_part_bytes(p->T, p->d_model, p->n_experts));
+    if (!dlogits || !x || !w_router || !dx || !dw_router || (need && !ws)) return MOE_ERR_NULL;
+    if (off_by(dlogits, 16) || off_by(x, 16) || off_by(w_router, 16) || off_by(dx_in, 16) || off_by(dx, 16) ||
+        off_by(dw_router, 16) || off_by(ws, 16) || dx == x)
+        return MOE_ERR_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = launched(launch_router_dx(p->act_dtype, dlogits, w_router, dx_in, nullptr, 1, dx, p->T, p->d_model,
+                                        p->n_experts, s))))
+        return st;
+    return launched(launch_router_dw(p->act_dtype, dlogits, x, static_cast<float*>(ws), dw_router, p->T, p->d_model,
+                                     p->n_experts, s));
+}
+
+// ----------------------------------------------------------------------------- a few tokens, 4-bit weights
+
+int32_t moe_decode_weight_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_decode(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = decode_packed(*p).total;
+    return MOE_OK;
+}
+
+int32_t moe_decode_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_decode(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = decode_layout(*p).total;
+    return MOE_OK;
+}
+
+int32_t moe_pack_weights_decode(const moe_problem* p, const void* w_gate, const void* w_up, const void* w_down,
+                                void* packed, void* stream) {
+    int32_t st = check_decode(p);
+    if (st) return st;
+    if (!w_gate || !w_up || !w_down || !packed) return MOE_ERR_NULL;
+    if (off_by(packed, 16)) return MOE_ERR_ARG;
+    const Packed P = decode_packed(*p);
+    auto u8 = [&](size_t off) { return reinterpret_cast<uint8_t*>(at(packed, off)); };
+    return launched(launch_pack_mxfp4(w_gate, w_up, w_down, u8(P.w1), u8(P.w2), u8(P.s1), u8(P.s2), p->n_experts,
+                                      p->d_model, p->d_hidden, static_cast<hipStream_t>(stream)));
+}
+
+static int32_t decode_experts_impl(const moe_problem* p, const void* x, const int32_t* idx, const float* gate,
+                                   const void* packed, void* y, void* ws, hipStream_t s) {
+    const Packed P = decode_packed(*p);
+    const DecodeLayout L = decode_layout(*p);
+    const uint8_t* pw = static_cast<const uint8_t*>(packed);
+    return launched(launch_decode_experts(static_cast<const uint16_t*>(x), idx, gate, pw + P.w1, pw + P.w2, pw + P.s1,
+                                          pw + P.s2, reinterpret_cast<uint16_t*>(at(ws, L.h)),
+                                          reinterpret_cast<float*>(at(ws, L.ye)), static_cast<uint16_t*>(y), p->T,
+                                          p->d_model, p->n_experts, p->top_k, p->d_hidden, s));
+}
+
+int32_t moe_decode_experts(const moe_problem* p, const void* x, const int32_t* topk_idx, const float* topk_gate,
+                           const void* packed, void* y, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_decode(p);
+    if (st) return st;
+    if (!x || !topk_idx || !topk_gate || !packed || !y || !ws) return MOE_ERR_NULL;
+    if (off_by(x, 16) || off_by(packed, 16) || off_by(y, 16) || off_by(ws, 16) || y == x) return MOE_ERR_ARG;
+    if (ws_bytes < decode_layout(*p).total) return MOE_ERR_WORKSPACE;
+    return decode_experts_impl(p, x, topk_idx, topk_gate, packed, y, ws, static_cast<hipStream_t>(stream));
+}
+
+int32_t moe_decode(const moe_problem* p, const void* x, const void* w_router, float* logits, const void* packed,
+                   void* y, int32_t* topk_idx, float* topk_gate, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_decode(p);
+    if (st) return st;
+    const bool given = p->flags & MOE_LOGITS_GIVEN;
+    if (!x || !logits || !packed || !y || !ws || (!given && !w_router)) return MOE_ERR_NULL;
+    if (off_by(x, 16) || off_by(w_router, 16) || off_by(logits, 16) || off_by(packed, 16) || off_by(y, 16) ||
+        off_by(ws, 16) || y == x)
+        return MOE_ERR_ARG;
+    const DecodeLayout L = decode_layout(*p);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    int32_t* idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(at(ws, L.idx));
+    float* gate = topk_gate ? topk_gate : reinterpret_cast<float*>(at(ws, L.gate));
+    if (!given && (st = launched(launch_router_logits(MOE_BF16, x, w_router, logits, p->T, p->d_model, p->n_experts,
+                                                      reinterpret_cast<uint16_t*>(at(ws, L.rwt)), s))))
+        return st;
+    if ((st = launched(launch_route_select(logits, p->T, p->n_experts, p->top_k, idx, gate,
+                                           reinterpret_cast<int32_t*>(at(ws, L.sel)), s))))
+        return st;
+    return decode_experts_impl(p, x, idx, gate, packed, y, ws, s);
 }
 
 }  // extern "C"

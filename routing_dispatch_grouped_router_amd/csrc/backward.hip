@@ -8,7 +8,9 @@
 //
 //   combine backward   dgate[t, j] = dy[t] . ye[pos[t, j]],  dye[pos[t, j]] = g[t, j] dy[t]
 //   router backward    dL[t, e_j] = g_j (dgate_j - sum_i g_i dgate_i), 0 elsewhere
-//                      (the gates are the softmax of the k selected logits)
+//                      (the gates are the softmax of the k selected logits);
+//                      with another loss's gradient for the logits that is added,
+//                      and the router's product is differentiated densely (router_bwd.hip)
 //   recompute          a | b = xe W1 (gate/up interleaved as packed), stored
 //   down dgrad         dh = dye W_down^T  (B operand: W_down [E][H][d] as given)
 //   SwiGLU backward    da = dh b silu'(a), db = dh silu(a), written over a | b
@@ -90,7 +92,8 @@ template <bool BF, int KMAX>
 __global__ __launch_bounds__(64 * kTokPerBlock) void combine_bwd_kernel(
     const void* __restrict__ dy, const void* __restrict__ ye, const float* __restrict__ gate,
     const int32_t* __restrict__ pos, const int32_t* __restrict__ idx, void* __restrict__ dye,
-    float* __restrict__ dL, float* __restrict__ dsel, float* __restrict__ srow, int T, int row_chunks, int E, int k) {
+    float* __restrict__ dL, float* __restrict__ dsel, float* __restrict__ srow, int T, int row_chunks, int E, int k,
+    const float* __restrict__ aux) {
     constexpr int NV = BF ? 8 : 4;
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * kTokPerBlock + (threadIdx.x >> 6);
@@ -165,7 +168,7 @@ __global__ __launch_bounds__(64 * kTokPerBlock) void combine_bwd_kernel(
 #pragma unroll
         for (int j = 0; j < KMAX; ++j)
             if (j < k && ex[j] == e) v = ds[j];
-        dL[(size_t)t * E + e] = v;
+        dL[(size_t)t * E + e] = aux != nullptr ? v + aux[(size_t)t * E + e] : v;
     }
 }
 
@@ -459,23 +462,23 @@ __global__ __launch_bounds__(256) void dq_mxfp8_kernel(const uint8_t* __restrict
 template <int KMAX>
 static void launch_combine_bwd_k(int act, const void* dy, const void* ye, const float* gate, const int32_t* pos,
                                  const int32_t* idx, void* dye, float* dL, float* dsel, float* srow, int T, int d,
-                                 int E, int k, hipStream_t s) {
+                                 int E, int k, hipStream_t s, const float* aux) {
     dim3 grid((T + kTokPerBlock - 1) / kTokPerBlock), block(64 * kTokPerBlock);
     if (act == kF32)
         hipLaunchKernelGGL((combine_bwd_kernel<false, KMAX>), grid, block, 0, s, dy, ye, gate, pos, idx, dye, dL,
-                           dsel, srow, T, d / 4, E, k);
+                           dsel, srow, T, d / 4, E, k, aux);
     else
         hipLaunchKernelGGL((combine_bwd_kernel<true, KMAX>), grid, block, 0, s, dy, ye, gate, pos, idx, dye, dL,
-                           dsel, srow, T, d / 8, E, k);
+                           dsel, srow, T, d / 8, E, k, aux);
 }
 
 hipError_t launch_combine_bwd(int act, const void* dy, const void* ye, const float* gate, const int32_t* pos,
                               const int32_t* idx, void* dye, float* dL, float* dsel, float* srow, int T, int d, int E,
-                              int k, hipStream_t s) {
-    if (k <= 2) launch_combine_bwd_k<2>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s);
-    else if (k <= 4) launch_combine_bwd_k<4>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s);
-    else if (k <= 8) launch_combine_bwd_k<8>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s);
-    else launch_combine_bwd_k<kMaxTopK>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s);
+                              int k, hipStream_t s, const float* aux) {
+    if (k <= 2) launch_combine_bwd_k<2>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s, aux);
+    else if (k <= 4) launch_combine_bwd_k<4>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s, aux);
+    else if (k <= 8) launch_combine_bwd_k<8>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s, aux);
+    else launch_combine_bwd_k<kMaxTopK>(act, dy, ye, gate, pos, idx, dye, dL, dsel, srow, T, d, E, k, s, aux);
     return hipGetLastError();
 }
 

@@ -12,6 +12,8 @@ namespace moe {
 constexpr int kRouteBlock = 256;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 16;
+// Most tokens of the decode form of the experts (MOE_DECODE_MAX_TOKENS).
+constexpr int kDecodeTokens = 256;
 
 enum Act { kF32 = 0, kBF16 = 1, kMXFP8 = 2 };
 
@@ -38,6 +40,11 @@ hipError_t launch_router_logits(int act, const void* x, const void* w, float* lo
 hipError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* topk_idx,
                              float* topk_gate, int32_t* rank, int32_t* hist, float* psum, float* ppart,
                              hipStream_t s);
+
+// The selection alone (topk_idx, topk_gate, bit for bit launch_route_topk's), for T <= kRouteBlock;
+// scratch holds T k + E int32.
+hipError_t launch_route_select(const float* logits, int T, int E, int k, int32_t* topk_idx, float* topk_gate,
+                               int32_t* scratch, hipStream_t s);
 
 // counts, offsets and base[nblk][E] = offsets[e] + tokens of earlier blocks routed to e;
 // with psum non-NULL also the router statistics stats[E + 2] (see route.hip); zero[0, nzero)
@@ -180,9 +187,10 @@ hipError_t launch_pack_w1t(int act, const void* w_gate, const void* w_up, void* 
 // dye[pos[t][j]] = gate[t][j] dy[t]; dL[T][E] (router gradient through the softmax of
 // the selected logits); dsel[t][j] = dL[t][idx[t][j]], and with srow non-NULL also
 // srow[pos[t][j]] = dsel[t][j] (T k floats, the router gradient of every routed row).
+// aux (optional, [T][E]) is added to dL (not to dsel or srow).
 hipError_t launch_combine_bwd(int act, const void* dy, const void* ye, const float* gate, const int32_t* pos,
                               const int32_t* idx, void* dye, float* dL, float* dsel, float* srow, int T, int d, int E,
-                              int k, hipStream_t s);
+                              int k, hipStream_t s, const float* aux = nullptr);
 
 // ab [R][2H] (a | b interleaved as packed W1) := da | db from dh [R][H].
 hipError_t launch_swiglu_bwd(int act, const void* dh, void* ab, int R, int H, hipStream_t s);
@@ -222,5 +230,43 @@ hipError_t launch_gemm_plain(int act, const void* A, const void* B, void* C, con
 // and up (32 + 32 per 64) and go to C (gate) or C2 (up) [e][m][N/2].
 hipError_t launch_wgrad_rows(int omap, const uint16_t* XA, const uint16_t* XB, const int32_t* offsets, int E, int M,
                              int N, float* C, float* C2, hipStream_t s);
+
+// ---------------------------------------------------------------- norm (norm.hip)
+
+// Per row: s = x + residual, rstd = (mean s^2 + eps)^-1/2, y = s rstd weight.  residual, sum, y,
+// rstd and q may be NULL; q (bf16 rows, d % 128 == 0): E4M3 codes [T][d] of y, q_scale dwords [T][d/128].
+hipError_t launch_norm(int act, const void* x, const void* residual, const void* weight, float eps, void* sum, void* y,
+                       void* q, uint8_t* q_scale, float* rstd, int T, int d, hipStream_t s);
+size_t norm_bwd_part_bytes(int act, int T, int d);
+hipError_t launch_norm_bwd(int act, const void* dy, const void* dsum, const void* s_in, const void* weight,
+                           const float* rstd, void* ds, float* dweight, float* part, int T, int d, hipStream_t s);
+
+// ---------------------------------------------------------------- balance loss (balance.hip)
+
+// Partial rows of the forward: part holds balance_blocks (E + 1) float, cnt as many int32.
+int balance_blocks(int T, int E);
+hipError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t* mask, int T, int E, int k,
+                          int32_t* counts, float* loss, float* part, int32_t* cnt, hipStream_t s);
+hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t* counts, const float* dloss,
+                              int T, int E, int k, float* dlogits, hipStream_t s);
+
+// ---------------------------------------------------------------- dense router gradients (router_bwd.hip)
+
+// dx[t] = a_t + dL[t] W_r^T, a_t = add[t] (pos NULL), the sum of add's rows pos[t][0 .. k), or 0 (add NULL).
+hipError_t launch_router_dx(int act, const float* dL, const void* w_router, const void* add, const int32_t* pos, int k,
+                            void* dx, int T, int d, int E, hipStream_t s);
+// dw_router = x^T dL; part: router_dw_part_bytes (may be 0) of scratch.
+size_t router_dw_part_bytes(int T, int d, int E);
+hipError_t launch_router_dw(int act, const float* dL, const void* x, float* part, float* dw_router, int T, int d,
+                            int E, hipStream_t s);
+
+// ---------------------------------------------------------------- few tokens, 4-bit weights (decode.hip)
+
+hipError_t launch_pack_mxfp4(const void* w_gate, const void* w_up, const void* w_down, uint8_t* w1, uint8_t* w2,
+                             uint8_t* s1, uint8_t* s2, int E, int d, int H, hipStream_t s);
+// T <= kDecodeTokens; h [T k][H] bfloat16 and ye [T k][d] float32 are scratch.
+hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const float* gate, const uint8_t* w1,
+                                 const uint8_t* w2, const uint8_t* s1, const uint8_t* s2, uint16_t* h, float* ye,
+                                 uint16_t* y, int T, int d, int E, int k, int H, hipStream_t s);
 
 }  // namespace moe

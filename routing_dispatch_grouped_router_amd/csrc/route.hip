@@ -572,6 +572,32 @@ hipError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* 
     return hipGetLastError();
 }
 
+// The selection without the ranks: G > 4 is the selection kernel alone; the
+// fused kernel of G <= 4 writes its one block's ranks and counts to scratch.
+template <int G>
+static void launch_select_only(const float* logits, int T, int E, int k, int32_t* topk_idx, float* topk_gate,
+                               int32_t* scratch, hipStream_t s) {
+    constexpr bool fuse = G <= 4;
+    constexpr int V = G == 64 ? 16 : 8, nthr = fuse ? kRouteBlock * G : kSelThreads, TA = nthr / G;
+    hipLaunchKernelGGL((route_select_kernel<G, V, fuse>), dim3((T + TA - 1) / TA), dim3(nthr), 0, s, logits, T, E, k,
+                       topk_idx, topk_gate, fuse ? scratch : nullptr, fuse ? scratch + (size_t)T * k : nullptr,
+                       static_cast<float*>(nullptr));
+}
+
+hipError_t launch_route_select(const float* logits, int T, int E, int k, int32_t* topk_idx, float* topk_gate,
+                               int32_t* scratch, hipStream_t s) {
+    switch (route_lanes(E)) {
+        case 1: launch_select_only<1>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+        case 2: launch_select_only<2>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+        case 4: launch_select_only<4>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+        case 8: launch_select_only<8>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+        case 16: launch_select_only<16>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+        case 32: launch_select_only<32>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+        default: launch_select_only<64>(logits, T, E, k, topk_idx, topk_gate, scratch, s); break;
+    }
+    return hipGetLastError();
+}
+
 // ----------------------------------------------------------------------------- scan
 
 // One workgroup of 1024 threads.  Thread (e, c) sums expert e's counts over a

@@ -13,11 +13,13 @@
 // operand, up to 16 routed rows the N operand of v_mfma_f32_16x16x32_bf16.  An
 // E2M1 value times a power of two is exact in bfloat16, so the weights are
 // converted in registers (v_cvt_scalef32_pk_bf16_fp4) without a rounding, and
-// the activations stay bfloat16.  A lane's 16-byte load is one scale block
-// (32 k of one row); the four MFMAs that consume it take k in the order the
-// lanes hold it, for both operands alike.  Rows are not sorted or moved: a
-// workgroup finds its expert's rows in topk_idx itself, and an index outside
-// [0, E) is a slot not in use.
+// the activations stay bfloat16.  Rows are not sorted or moved: a workgroup
+// finds its expert's rows in topk_idx itself, and an index outside [0, E) is a
+// slot not in use.
+//
+// Every sum over K is taken in four quarters (of K / 128 slices, in order) that
+// are added in order, whichever kernel and however many rows: a token's result
+// does not depend on the tokens beside it.
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -26,6 +28,12 @@ namespace moe {
 namespace {
 
 constexpr int kMaxRows = kDecodeTokens * kMaxTopK;
+
+// This wave's index, and a value that is the same on all its lanes, known to be
+// uniform: the branches around the MFMAs (which ignore the lane mask) have to
+// be scalar ones.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int wave_index() { return uniform((int)(threadIdx.x >> 6)); }
 
 __device__ __forceinline__ float e8m0_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
@@ -38,115 +46,255 @@ __device__ __forceinline__ bf16x8 fp4_to_bf16(uint32_t w, float scale) {
     return (bf16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Row list of a group: LDS for every routed row.
+struct GroupRows {
+    uint16_t rows[kMaxRows];
+    int32_t cnt[4];
+};
+
 // The routed rows of group g: with R <= E a group per routed row, whose rows
 // are those of its expert if it is the expert's first row (none otherwise);
 // else a group per expert.  rows[0, n) in ascending order; returns n, the
 // same on every thread of the workgroup's 256.
-__device__ __forceinline__ int group_rows(const int32_t* idx, int R, int E, int g, int& expert, int32_t* rows,
-                                          int32_t* wcnt) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    expert = R <= E ? idx[g] : g;
-    if (expert < 0 || expert >= E) return 0;   // uniform
+__device__ __forceinline__ int group_rows(const int32_t* idx, int R, int E, int g, int& expert, GroupRows& s) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+    if (R <= 64) {   // one load; every wave writes the same list and reads its own writes
+        const int mine = lane < R ? idx[lane] : -1;
+        expert = R <= E ? uniform(__shfl(mine, g)) : g;
+        if (expert < 0 || expert >= E) return 0;
+        const uint64_t b = __ballot(mine == expert);
+        if (R <= E && __ffsll((unsigned long long)b) - 1 != g) return 0;   // another row of this expert comes first
+        if (mine == expert) s.rows[__popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)lane;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        return __popcll(b);
+    }
+    expert = R <= E ? uniform(idx[g]) : g;
+    if (expert < 0 || expert >= E) return 0;
     int n = 0;
     for (int base = 0; base < R; base += 256) {
         const int r = base + tid;
         const bool mine = r < R && idx[r] == expert;
         const uint64_t b = __ballot(mine);
-        if (lane == 0) wcnt[wave] = __popcll(b);
+        if (lane == 0) s.cnt[wave] = __popcll(b);
         __syncthreads();
         int off = n, all = n;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (w < wave) off += wcnt[w];
-            all += wcnt[w];
+            if (w < wave) off += s.cnt[w];
+            all += s.cnt[w];
         }
-        if (mine) rows[off + __popcll(b & ((1ull << lane) - 1ull))] = r;
-        n = all;
-        __syncthreads();   // wcnt is rewritten by the next 256 rows; rows[] is complete after the last
+        if (mine) s.rows[off + __popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)r;
+        n = uniform(all);
+        __syncthreads();   // cnt is rewritten by the next 256 rows; rows[] is complete after the last
     }
-    if (R <= E && rows[0] != g) return 0;      // uniform: another row of this expert comes first
+    if (R <= E && uniform(s.rows[0]) != g) return 0;   // another row of this expert comes first
     return n;
 }
 
-// NB blocks of 16 weight rows (row0[b] their first row's codes, srow0[b] its
-// scales) times 16 routed rows (lane l: row l % 16 at xrow, zero unless live),
-// over the 128-wide slices [s0, s1) of K.
+// What a wave streams: NB blocks of 16 weight rows against 16 routed rows.
+// The memory pipe takes one access a clock for four consecutive lanes of one
+// 64-byte piece, but for every lane of its own row if the lanes are laid out
+// as the MFMA operands need them (rows across consecutive lanes: 390 accesses
+// a slice, and the kernel ran at that pipe's rate, 2.7 TB/s).  So four lanes
+// load 64 bytes of a weight row, sixteen 256 bytes of an activation row, and
+// the operands are gathered through a wave-private LDS stage (no barrier: one
+// wave writes and reads it, in order).
+//   w : chunk c (16 bytes, one scale block) of row r at 4 r + (c + r / 4) % 4
+//   x : chunk c (8 values) of row r at 16 r + (c ^ r)
+// which spreads the 16 rows of an operand read over all banks.
 template <int NB>
-__device__ __forceinline__ void mma_slices(const uint8_t* const (&wrow)[NB], const uint8_t* const (&srow)[NB],
-                                           const uint16_t* xrow, bool live, int s0, int s1, f32x4 (&acc)[NB]) {
-    const int q = (threadIdx.x & 63) >> 4;
-    constexpr int U = 2;   // slices in flight
-    for (int s = s0; s < s1; s += U) {
-        u32x4 w[U][NB], xv[U][4];
-        uint32_t sc[U][NB];
+struct Stage {
+    u32x4 w[NB][64];
+    u32x4 x[256];
+    uint32_t sc[NB * 16 * 8];   // scale dwords of 8 slices, [row][slice]
+};
+
+constexpr int kAhead = 4;       // slices of weights in flight
+
+// A lane's addresses of the weights (row lane / 4 of each block) and scales.
+template <int NB>
+struct Weights {
+    const uint8_t* w[NB];
+    const uint8_t* s[2 * NB];
+};
+
+// Blocks at rows row0[b] .. + 16 of codes [.][K / 2] and scales [.][K / 32].
+template <int NB>
+__device__ __forceinline__ Weights<NB> weights_at(const uint8_t* w, const uint8_t* s, const size_t (&row0)[NB], int K) {
+    const int lane = threadIdx.x & 63;
+    Weights<NB> p;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int sl = min(s + u, s1 - 1);   // a clamped slice is loaded, not used
+    for (int b = 0; b < NB; ++b) {
+        p.w[b] = w + (row0[b] + (lane >> 2)) * (size_t)(K / 2) + 16 * (((lane & 3) - (lane >> 4)) & 3);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                w[u][b] = *reinterpret_cast<const u32x4*>(wrow[b] + 64 * sl + 16 * q);
-                sc[u][b] = srow[b][4 * sl + q];
-            }
+        for (int i = 0; i < 2; ++i)   // entry lane + 64 i of the block's [16][8] scale dwords
+            p.s[2 * b + i] = s + (row0[b] + 8 * i + (lane >> 3)) * (size_t)(K / 32);
+    }
+    return p;
+}
+
+// The first slices' weights and scales, [s0, s1), requested ahead of their use.
+template <int NB>
+struct Ahead {
+    u32x4 w[kAhead][NB];
+    uint32_t sc[2 * NB];
+};
+
+template <int NB>
+__device__ __forceinline__ void load_scales(const Weights<NB>& p, int s, int s1, uint32_t (&sc)[2 * NB]) {
+    const int sl = min(s + (int)(threadIdx.x & 7), s1 - 1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xv[u][i] = *reinterpret_cast<const u32x4*>(xrow + 128 * sl + 32 * q + 8 * i);
+    for (int i = 0; i < 2 * NB; ++i) sc[i] = *reinterpret_cast<const uint32_t*>(p.s[i] + 4 * sl);
+}
+
+template <int NB>
+__device__ __forceinline__ void load_ahead(const Weights<NB>& p, int s0, int s1, Ahead<NB>& a) {
+    if (s0 >= s1) return;
+    load_scales<NB>(p, s0, s1, a.sc);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (s0 + u < s1) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) a.w[u][b] = *reinterpret_cast<const u32x4*>(p.w[b] + 64 * (s0 + u));
         }
+}
+
+// A lane's addresses of the activation rows: chunk lane % 16 of rows
+// 4 j + lane / 16, j < nx.  Columns past the last row repeat it (or hold
+// what the stage held): the columns of the product are independent, and theirs
+// are not stored.
+struct Acts {
+    const uint16_t* x[4];
+    int nx;
+};
+
+// acc[b] = the product over the 128-wide slices [s0, s1) of K, on top of acc.
+template <int NB>
+__device__ __forceinline__ void mma_slices(Stage<NB>& st, const Weights<NB>& p, Ahead<NB>& a, const Acts& in, int s0,
+                                           int s1, f32x4 (&acc)[NB]) {
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    u32x4 x[2][4];
+    auto load_x = [&](int sl, u32x4 (&v)[4]) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s + u >= s1) continue;
+        for (int j = 0; j < 4; ++j)
+            if (j < in.nx) v[j] = *reinterpret_cast<const u32x4*>(in.x[j] + 128 * sl);
+    };
+    if (s0 < s1) load_x(s0, x[0]);
+    if (s0 + 1 < s1) load_x(s0 + 1, x[1]);
+    for (int g = s0; g < s1; g += 8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, live ? xv[u][i] : (u32x4){0u, 0u, 0u, 0u});
+        for (int i = 0; i < 2 * NB; ++i) st.sc[lane + 64 * i] = a.sc[i];
+        if (g + 8 < s1) load_scales<NB>(p, g + 8, s1, a.sc);
+        for (int h = g; h < min(g + 8, s1); h += kAhead) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4_to_bf16(w[u][b][i], e8m0_scale(sc[u][b])), x,
-                                                                     acc[b], 0, 0, 0);
+            for (int u = 0; u < kAhead; ++u) {
+                const int s = h + u;
+                if (s >= s1) break;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) st.w[b][lane] = a.w[u][b];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < in.nx) st.x[64 * j + 16 * q + (m ^ (4 * j + q))] = x[u & 1][j];
+                if (s + kAhead < s1) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        a.w[u][b] = *reinterpret_cast<const u32x4*>(p.w[b] + 64 * (s + kAhead));
+                }
+                if (s + 2 < s1) load_x(s + 2, x[u & 1]);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                u32x4 wf[NB], xf[4];
+                float sc[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    wf[b] = st.w[b][4 * m + ((q + (m >> 2)) & 3)];
+                    sc[b] = e8m0_scale(reinterpret_cast<const uint8_t*>(st.sc)[((16 * b + m) * 8 + (s - g)) * 4 + q]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xf[i] = st.x[16 * m + ((4 * q + i) ^ m)];
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4_to_bf16(wf[b][i], sc[b]),
+                                                                         __builtin_bit_cast(bf16x8, xf[i]), acc[b], 0,
+                                                                         0, 0);
             }
         }
+    }
+}
+
+// Rows rows[n0 .. n) of a list as a wave's activations: row r reads line
+// r / div of x [.][K].
+__device__ __forceinline__ Acts acts_at(const uint16_t* x, const uint16_t* rows, int n0, int n, int div, int K) {
+    const int lane = threadIdx.x & 63;
+    Acts in;
+    in.nx = min(4, (n - n0 + 3) / 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        in.x[j] = x + (size_t)(rows[min(n0 + 4 * j + (lane >> 4), n - 1)] / div) * K + 8 * (lane & 15);
+    return in;
+}
+
+// Two blocks of 16 weight rows (row0) times the group's rows, the waves of the
+// workgroup taking the quarters of K: the quarters' sums of rows n0 .. + 16,
+// added in order, to store(routed row, block 0, block 1) on wave 0's lanes.
+template <typename Store>
+__device__ __forceinline__ void group_product(GroupRows& s_g, Stage<2>* stage, const uint8_t* w, const uint8_t* s,
+                                              const size_t (&row0)[2], const uint16_t* x, int n, int div, int K,
+                                              Store store) {
+    const int lane = threadIdx.x & 63, wave = wave_index(), m = lane & 15;
+    const int ns = K / 128, sl0 = wave * ns / 4, sl1 = (wave + 1) * ns / 4;
+    const Weights<2> p = weights_at<2>(w, s, row0, K);
+    for (int n0 = 0; n0 < n; n0 += 16) {
+        Ahead<2> a;
+        load_ahead<2>(p, sl0, sl1, a);
+        const Acts in = acts_at(x, s_g.rows, n0, n, div, K);
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        mma_slices<2>(stage[wave], p, a, in, sl0, sl1, acc);
+        f32x4* red = reinterpret_cast<f32x4*>(stage[wave].x);
+        red[lane] = acc[0];
+        red[64 + lane] = acc[1];
+        __syncthreads();
+        if (wave == 0 && n0 + m < n) {
+            f32x4 v[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                auto part = [&](int i) { return reinterpret_cast<const f32x4*>(stage[i].x)[64 * b + lane]; };
+                v[b] = ((part(0) + part(1)) + part(2)) + part(3);
+            }
+            store((int)s_g.rows[n0 + m], v[0], v[1]);
+        }
+        if (n0 + 16 < n) __syncthreads();   // the stages are written again
     }
 }
 
 }  // namespace
 
-// Gate and up projections: workgroup = (group, 16 hidden units).  Its four
-// waves take the quarters of d; wave 0 adds them in order and stores
-// h = silu(a) b, bfloat16, at h[r][H].
+// Gate and up projections: workgroup = (group, 16 hidden units);
+// h[r] = silu(a) b as bfloat16.
 __global__ __launch_bounds__(256) void decode_up_kernel(const uint16_t* __restrict__ x,
                                                         const int32_t* __restrict__ idx,
                                                         const uint8_t* __restrict__ w1,
                                                         const uint8_t* __restrict__ s1, uint16_t* __restrict__ h,
                                                         int R, int E, int k, int d, int H) {
-    __shared__ int32_t s_rows[kMaxRows];
-    __shared__ int32_t s_cnt[4];
-    __shared__ f32x4 red[4][2][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
+    __shared__ GroupRows s_g;
+    __shared__ Stage<2> stage[4];
     const int nb = H / 16, g = blockIdx.x / nb, hb = blockIdx.x - g * nb;
     int e;
-    const int n = group_rows(idx, R, E, g, e, s_rows, s_cnt);
+    const int n = group_rows(idx, R, E, g, e, s_g);
     if (n == 0) return;
     // packed rows of hidden units 16 hb .. + 16: gate at 64 (hb / 2) + 16 (hb % 2), up 32 further
-    const size_t row = (size_t)e * 2 * H + 64 * (hb >> 1) + 16 * (hb & 1) + m;
-    const uint8_t* const wrow[2] = {w1 + row * (d / 2), w1 + (row + 32) * (d / 2)};
-    const uint8_t* const srow[2] = {s1 + row * (d / 32), s1 + (row + 32) * (d / 32)};
-    const int ns = d / 128, sl0 = wave * ns / 4, sl1 = (wave + 1) * ns / 4;
-    for (int n0 = 0; n0 < n; n0 += 16) {
-        const bool live = n0 + m < n;
-        const int r = s_rows[min(n0 + m, n - 1)];
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        mma_slices<2>(wrow, srow, x + (size_t)(r / k) * d, live, sl0, sl1, acc);
-        red[wave][0][lane] = acc[0];
-        red[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (wave == 0 && live) {
-            const f32x4 a = ((red[0][0][lane] + red[1][0][lane]) + red[2][0][lane]) + red[3][0][lane];
-            const f32x4 b = ((red[0][1][lane] + red[1][1][lane]) + red[2][1][lane]) + red[3][1][lane];
-            float o[4];
+    const size_t row = (size_t)e * 2 * H + 64 * (hb >> 1) + 16 * (hb & 1);
+    const int q = (threadIdx.x & 63) >> 4;
+    group_product(s_g, stage, w1, s1, {row, row + 32}, x, n, k, d, [&](int r, const f32x4& a, const f32x4& b) {
+        float o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-            *reinterpret_cast<uint2*>(h + (size_t)r * H + 16 * hb + 4 * q) =
-                make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-        }
-        __syncthreads();   // red is rewritten for the next rows
-    }
+        for (int i = 0; i < 4; ++i) o[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
+        *reinterpret_cast<uint2*>(h + (size_t)r * H + 16 * hb + 4 * q) =
+            make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    });
 }
 
 // Down projection: workgroup = (group, 32 outputs), ye[r][d] in float32.
@@ -155,60 +303,91 @@ __global__ __launch_bounds__(256) void decode_down_kernel(const uint16_t* __rest
                                                           const uint8_t* __restrict__ w2,
                                                           const uint8_t* __restrict__ s2, float* __restrict__ ye,
                                                           int R, int E, int d, int H) {
-    __shared__ int32_t s_rows[kMaxRows];
-    __shared__ int32_t s_cnt[4];
-    __shared__ f32x4 red[4][2][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
+    __shared__ GroupRows s_g;
+    __shared__ Stage<2> stage[4];
     const int nb = d / 32, g = blockIdx.x / nb, cb = blockIdx.x - g * nb;
     int e;
-    const int n = group_rows(idx, R, E, g, e, s_rows, s_cnt);
+    const int n = group_rows(idx, R, E, g, e, s_g);
     if (n == 0) return;
-    const size_t row = (size_t)e * d + 32 * cb + m;
-    const uint8_t* const wrow[2] = {w2 + row * (H / 2), w2 + (row + 16) * (H / 2)};
-    const uint8_t* const srow[2] = {s2 + row * (H / 32), s2 + (row + 16) * (H / 32)};
-    const int ns = H / 128, sl0 = wave * ns / 4, sl1 = (wave + 1) * ns / 4;
-    for (int n0 = 0; n0 < n; n0 += 16) {
-        const bool live = n0 + m < n;
-        const int r = s_rows[min(n0 + m, n - 1)];
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        mma_slices<2>(wrow, srow, h + (size_t)r * H, live, sl0, sl1, acc);
-        red[wave][0][lane] = acc[0];
-        red[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (wave < 2 && live)   // wave b stores block b's outputs 32 cb + 16 b + 4 q .. + 4
-            *reinterpret_cast<f32x4*>(ye + (size_t)r * d + 32 * cb + 16 * wave + 4 * q) =
-                ((red[0][wave][lane] + red[1][wave][lane]) + red[2][wave][lane]) + red[3][wave][lane];
-        __syncthreads();
-    }
+    const size_t row = (size_t)e * d + 32 * cb;
+    const int q = (threadIdx.x & 63) >> 4;
+    group_product(s_g, stage, w2, s2, {row, row + 16}, h, n, 1, H, [&](int r, const f32x4& a, const f32x4& b) {
+        float* dst = ye + (size_t)r * d + 32 * cb + 4 * q;
+        *reinterpret_cast<f32x4*>(dst) = a;
+        *reinterpret_cast<f32x4*>(dst + 16) = b;
+    });
 }
 
 // y[t] = sum_j gate[t][j] ye[t k + j] in slot order over the slots in use
-// (float32, rounded once); four outputs per thread.
+// (float32, rounded once); four outputs per thread.  Slots past k repeat slot
+// k - 1, so that the loads need no branch and are in flight together.
+template <int KMAX>
 __global__ __launch_bounds__(256) void decode_combine_kernel(const float* __restrict__ ye,
                                                              const int32_t* __restrict__ idx,
                                                              const float* __restrict__ gate, uint16_t* __restrict__ y,
                                                              int E, int k, int d) {
     const int t = blockIdx.y, c = 4 * (blockIdx.x * 256 + threadIdx.x);
     if (c >= d) return;
-    f32x4 v[kMaxTopK];
-    float g[kMaxTopK];
+    f32x4 v[KMAX];
+    float g[KMAX];
+    int e[KMAX];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-        g[j] = 0.f;
-        v[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        if (j < k) {
-            const int e = idx[t * k + j];
-            if (e >= 0 && e < E) {
-                g[j] = gate[t * k + j];
-                v[j] = *reinterpret_cast<const f32x4*>(ye + ((size_t)t * k + j) * d + c);
-            }
-        }
+    for (int j = 0; j < KMAX; ++j) {
+        const int r = t * k + min(j, k - 1);
+        e[j] = idx[r];
+        g[j] = gate[r];
+        v[j] = *reinterpret_cast<const f32x4*>(ye + (size_t)r * d + c);
     }
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j)
-        if (j < k) s += g[j] * v[j];
+    for (int j = 0; j < KMAX; ++j) {
+        if (j < k && e[j] >= 0 && e[j] < E) {   // ye of an unused slot was not written
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = fmaf(g[j], v[j][i], s[i]);
+        }
+    }
     *reinterpret_cast<uint2*>(y + (size_t)t * d + c) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+}
+
+// Down projection and combine of few rows: workgroup = (token, 16 outputs),
+// sixteen waves, a wave per quarter of a slot in turn (the slot's h the only
+// column).  No float32 rows and no third launch, but tokens that share an
+// expert each read its weights.
+__global__ __launch_bounds__(1024) void decode_down_token_kernel(const uint16_t* __restrict__ h,
+                                                                 const int32_t* __restrict__ idx,
+                                                                 const float* __restrict__ gate,
+                                                                 const uint8_t* __restrict__ w2,
+                                                                 const uint8_t* __restrict__ s2,
+                                                                 uint16_t* __restrict__ y, int E, int k, int d, int H) {
+    __shared__ Stage<1> stage[16];
+    __shared__ float red[kMaxTopK][4][16];
+    __shared__ float s_gate[kMaxTopK];
+    const int lane = threadIdx.x & 63, wave = wave_index(), m = lane & 15, q = lane >> 4;
+    const int nb = d / 16, t = blockIdx.x / nb, cb = blockIdx.x - t * nb;
+    const int ns = H / 128;
+    for (int u = wave; u < 4 * k; u += 16) {
+        const int j = u >> 2, quarter = u & 3, r = t * k + j, e = uniform(idx[r]);
+        const bool used = e >= 0 && e < E;
+        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        if (used) {
+            const int sl0 = quarter * ns / 4, sl1 = (quarter + 1) * ns / 4;
+            const Weights<1> p = weights_at<1>(w2, s2, {(size_t)e * d + 16 * cb}, H);
+            Ahead<1> a;
+            load_ahead<1>(p, sl0, sl1, a);
+            const uint16_t* hr = h + (size_t)r * H + 8 * m;
+            mma_slices<1>(stage[wave], p, a, {{hr, hr, hr, hr}, 1}, sl0, sl1, acc);
+        }
+        if (m == 0) *reinterpret_cast<f32x4*>(&red[j][quarter][4 * q]) = acc[0];
+        if (lane == 0 && quarter == 0) s_gate[j] = used ? gate[r] : 0.f;
+    }
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        const int c = threadIdx.x;
+        float s = 0.f;
+        for (int j = 0; j < k; ++j)
+            s = fmaf(s_gate[j], ((red[j][0][c] + red[j][1][c]) + red[j][2][c]) + red[j][3][c], s);
+        y[(size_t)t * d + 16 * cb + c] = f32_to_bf16(s);
+    }
 }
 
 // E2M1 code of v: round to nearest even, saturate to +-6, keep the sign on zero.
@@ -268,8 +447,16 @@ hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const fl
                                  uint16_t* y, int T, int d, int E, int k, int H, hipStream_t s) {
     const int R = T * k, G = R <= E ? R : E;
     hipLaunchKernelGGL(decode_up_kernel, dim3(G * (H / 16)), dim3(256), 0, s, x, idx, w1, s1, h, R, E, k, d, H);
+    if (2 * R <= E) {
+        hipLaunchKernelGGL(decode_down_token_kernel, dim3(T * (d / 16)), dim3(1024), 0, s, h, idx, gate, w2, s2, y, E, k,
+                           d, H);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(decode_down_kernel, dim3(G * (d / 32)), dim3(256), 0, s, h, idx, w2, s2, ye, R, E, d, H);
-    hipLaunchKernelGGL(decode_combine_kernel, dim3((d / 4 + 255) / 256, T), dim3(256), 0, s, ye, idx, gate, y, E, k, d);
+    const dim3 cg((d / 4 + 255) / 256, T), cb(256);
+    if (k <= 4) hipLaunchKernelGGL(decode_combine_kernel<4>, cg, cb, 0, s, ye, idx, gate, y, E, k, d);
+    else if (k <= 8) hipLaunchKernelGGL(decode_combine_kernel<8>, cg, cb, 0, s, ye, idx, gate, y, E, k, d);
+    else hipLaunchKernelGGL(decode_combine_kernel<kMaxTopK>, cg, cb, 0, s, ye, idx, gate, y, E, k, d);
     return hipGetLastError();
 }
 

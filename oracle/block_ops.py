@@ -105,9 +105,9 @@ def decode_weights(packed, E, d, H):
     return gate, up, np.ascontiguousarray(w2.swapaxes(1, 2))
 
 
-def decode_experts(x, idx, gate, wg, wu, wd, u_h=2.0 ** -8):
+def decode_experts(x, idx, gate, wg, wu, wd, u_h=2.0 ** -16):
     """(y, bound): y[t] = sum_j gate FFN(x[t]), and how far float32 sums with h
-    stored in bfloat16 can be from it before y itself is rounded: with u the
+    stored to u_h of it (as two bfloat16 terms) can be from it before y itself is rounded: with u the
     float32 half-step, a sum of n products is off by at most n u times the sum
     of their magnitudes; |silu'| < 1.1."""
     u = 2.0 ** -24

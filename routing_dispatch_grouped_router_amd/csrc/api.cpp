@@ -221,6 +221,9 @@ int32_t check_decode(const moe_problem* p) {
     if (st) return st;
     if (p->act_dtype == MOE_F32 || (p->flags & MOE_IDENTITY_EXPERTS)) return MOE_ERR_DTYPE;
     if (p->T > MOE_DECODE_MAX_TOKENS || p->d_model % 128 || p->d_hidden % 128) return MOE_ERR_SHAPE;
+    // x [T][d] and h [T k][2][H] are addressed with 32-bit byte offsets (bfloat16 for either act_dtype)
+    if ((long long)p->T * p->top_k * std::max<long long>(p->d_model, 2LL * p->d_hidden) * 2 >= (1LL << 32))
+        return MOE_ERR_SHAPE;
     return MOE_OK;
 }
 static_assert(kDecodeTokens == MOE_DECODE_MAX_TOKENS && kDecodeTokens <= kRouteBlock, "one routing block");
@@ -246,7 +249,7 @@ DecodeLayout decode_layout(const moe_problem& p) {
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off += align256(bytes); return o; };
     const size_t R = (size_t)p.T * p.top_k, E = p.n_experts, d = p.d_model;
-    L.h = take(R * p.d_hidden * 2);
+    L.h = take(R * p.d_hidden * 4);   // two bfloat16 terms
     L.ye = take(R * d * 4);
     L.idx = take(R * 4);
     L.gate = take(R * 4);

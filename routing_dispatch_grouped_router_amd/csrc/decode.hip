@@ -13,7 +13,11 @@
 // operand, up to 16 routed rows the N operand of v_mfma_f32_16x16x32_bf16.  An
 // E2M1 value times a power of two is exact in bfloat16, so the weights are
 // converted in registers (v_cvt_scalef32_pk_bf16_fp4) without a rounding, and
-// the activations stay bfloat16.  Rows are not sorted or moved: a workgroup
+// x stays bfloat16.  h goes through memory as two bfloat16 terms (the rounded
+// value and the rounded remainder, 2^-16 of it left out): rounded once it would
+// add as much error to y as y's own rounding, and the second term costs loads
+// that hit the caches and matrix instructions that the weights' bytes hide.
+// Rows are not sorted or moved: a workgroup
 // finds its expert's rows in topk_idx itself, and an index outside [0, E) is a
 // slot not in use.
 //
@@ -49,7 +53,7 @@ __device__ __forceinline__ bf16x8 fp4_to_bf16(uint32_t w, float scale) {
 // Row list of a group: LDS for every routed row.
 struct GroupRows {
     uint16_t rows[kMaxRows];
-    int32_t cnt[4];
+    int32_t cnt[4][4];
 };
 
 // The routed rows of group g: with R <= E a group per routed row, whose rows
@@ -72,21 +76,30 @@ __device__ __forceinline__ int group_rows(const int32_t* idx, int R, int E, int 
     expert = R <= E ? uniform(idx[g]) : g;
     if (expert < 0 || expert >= E) return 0;
     int n = 0;
-    for (int base = 0; base < R; base += 256) {
-        const int r = base + tid;
-        const bool mine = r < R && idx[r] == expert;
-        const uint64_t b = __ballot(mine);
-        if (lane == 0) s.cnt[wave] = __popcll(b);
-        __syncthreads();
-        int off = n, all = n;
+    for (int base = 0; base < R; base += 1024) {   // 1024 rows at a time: their loads together, two barriers
+        int v[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w < wave) off += s.cnt[w];
-            all += s.cnt[w];
+        for (int i = 0; i < 4; ++i) v[i] = base + 256 * i < R ? idx[min(base + 256 * i + tid, R - 1)] : -1;
+        uint64_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[i] = __ballot(v[i] == expert && base + 256 * i + tid < R);
+            if (lane == 0) s.cnt[i][wave] = __popcll(b[i]);
         }
-        if (mine) s.rows[off + __popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)r;
-        n = uniform(all);
-        __syncthreads();   // cnt is rewritten by the next 256 rows; rows[] is complete after the last
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int off = n, all = n;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int c = s.cnt[i][w];
+                if (w < wave) off += c;
+                all += c;
+            }
+            if (b[i] >> lane & 1) s.rows[off + __popcll(b[i] & ((1ull << lane) - 1ull))] = (uint16_t)(base + 256 * i + tid);
+            n = uniform(all);
+        }
+        __syncthreads();   // cnt is rewritten by the next rows; rows[] is complete after the last
     }
     if (R <= E && uniform(s.rows[0]) != g) return 0;   // another row of this expert comes first
     return n;
@@ -103,41 +116,59 @@ __device__ __forceinline__ int group_rows(const int32_t* idx, int R, int E, int 
 //   w : chunk c (16 bytes, one scale block) of row r at 4 r + (c + r / 4) % 4
 //   x : chunk c (8 values) of row r at 16 r + (c ^ r)
 // which spreads the 16 rows of an operand read over all banks.
-template <int NB>
+// XR rows of activations are staged (1, 4 or 16), each of NT terms (row r of
+// term n at XR n + r); column m of the product reads row m % XR.
+template <int NB, int XR, int NT>
 struct Stage {
     u32x4 w[NB][64];
-    u32x4 x[256];
+    u32x4 x[16 * XR * NT];
     uint32_t sc[NB * 16 * 8];   // scale dwords of 8 slices, [row][slice]
 };
 
-constexpr int kAhead = 4;       // slices of weights in flight
+// 16 bytes or a dword at a uniform address plus a lane's 32-bit offset (an
+// expert's weights and an activation buffer are below 2^32 bytes).
+__device__ __forceinline__ u32x4 load16(const uint8_t* base, uint32_t off) {
+    return *reinterpret_cast<const u32x4*>(base + off);
+}
+__device__ __forceinline__ uint32_t load4(const uint8_t* base, uint32_t off) {
+    return *reinterpret_cast<const uint32_t*>(base + off);
+}
 
-// A lane's addresses of the weights (row lane / 4 of each block) and scales.
+// Weight rows row0[b] .. + 16 of an expert's codes w [.][K / 2] and scales
+// s [.][K / 32], and a lane's offsets: row lane / 4 of each block's codes,
+// entries lane and lane + 64 of its [16][8] scale dwords (rows lane / 8 and
+// 8 further).
 template <int NB>
 struct Weights {
-    const uint8_t* w[NB];
-    const uint8_t* s[2 * NB];
+    const uint8_t* w;
+    const uint8_t* s;
+    uint32_t wo[NB], so[2 * NB];
 };
 
-// Blocks at rows row0[b] .. + 16 of codes [.][K / 2] and scales [.][K / 32].
 template <int NB>
-__device__ __forceinline__ Weights<NB> weights_at(const uint8_t* w, const uint8_t* s, const size_t (&row0)[NB], int K) {
+__device__ __forceinline__ Weights<NB> weights_at(const uint8_t* w, const uint8_t* s, const int (&row0)[NB], int K) {
     const int lane = threadIdx.x & 63;
     Weights<NB> p;
+    p.w = w;
+    p.s = s;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        p.w[b] = w + (row0[b] + (lane >> 2)) * (size_t)(K / 2) + 16 * (((lane & 3) - (lane >> 4)) & 3);
+        p.wo[b] = (uint32_t)(row0[b] + (lane >> 2)) * (uint32_t)(K / 2) + 16 * (((lane & 3) - (lane >> 4)) & 3);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)   // entry lane + 64 i of the block's [16][8] scale dwords
-            p.s[2 * b + i] = s + (row0[b] + 8 * i + (lane >> 3)) * (size_t)(K / 32);
+        for (int i = 0; i < 2; ++i) p.so[2 * b + i] = (uint32_t)(row0[b] + 8 * i + (lane >> 3)) * (uint32_t)(K / 32);
     }
     return p;
 }
 
-// The first slices' weights and scales, [s0, s1), requested ahead of their use.
-template <int NB>
+// Loads of an activation slice: four staged rows each.
+constexpr int x_loads(int XR, int NT) { return (XR * NT + 3) / 4; }
+
+// Requests in flight: D slices of weights and of activations (loads return in
+// order, so a slice of one kind waits for those of the other requested before
+// it: both have the same depth), and the next 8 slices' scales.
+template <int NB, int XR, int NT, int D>
 struct Ahead {
-    u32x4 w[kAhead][NB];
+    u32x4 w[D][NB], x[D][x_loads(XR, NT)];
     uint32_t sc[2 * NB];
 };
 
@@ -145,176 +176,222 @@ template <int NB>
 __device__ __forceinline__ void load_scales(const Weights<NB>& p, int s, int s1, uint32_t (&sc)[2 * NB]) {
     const int sl = min(s + (int)(threadIdx.x & 7), s1 - 1);
 #pragma unroll
-    for (int i = 0; i < 2 * NB; ++i) sc[i] = *reinterpret_cast<const uint32_t*>(p.s[i] + 4 * sl);
+    for (int i = 0; i < 2 * NB; ++i) sc[i] = load4(p.s, p.so[i] + 4 * sl);
 }
 
-template <int NB>
-__device__ __forceinline__ void load_ahead(const Weights<NB>& p, int s0, int s1, Ahead<NB>& a) {
-    if (s0 >= s1) return;
-    load_scales<NB>(p, s0, s1, a.sc);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        if (s0 + u < s1) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) a.w[u][b] = *reinterpret_cast<const u32x4*>(p.w[b] + 64 * (s0 + u));
-        }
-}
-
-// A lane's addresses of the activation rows: chunk lane % 16 of rows
-// 4 j + lane / 16, j < nx.  Columns past the last row repeat it (or hold
-// what the stage held): the columns of the product are independent, and theirs
-// are not stored.
+// Activation rows: a lane's offsets of chunk lane % 16 of staged rows
+// 4 j + lane / 16.  Of a term's loads the first nx have a row to bring (XR < 16:
+// all).  Columns past the last row repeat it (or hold what the stage held): the
+// columns of the product are independent, and theirs are not stored.
+template <int XR, int NT>
 struct Acts {
-    const uint16_t* x[4];
+    const uint8_t* x;
+    uint32_t xo[x_loads(XR, NT)];
     int nx;
 };
 
-// acc[b] = the product over the 128-wide slices [s0, s1) of K, on top of acc.
-template <int NB>
-__device__ __forceinline__ void mma_slices(Stage<NB>& st, const Weights<NB>& p, Ahead<NB>& a, const Acts& in, int s0,
-                                           int s1, f32x4 (&acc)[NB]) {
-    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    u32x4 x[2][4];
-    auto load_x = [&](int sl, u32x4 (&v)[4]) {
+template <int XR>
+__device__ __forceinline__ bool brings(int j, int nx) {
+    return XR < 16 || j % (XR / 4) < nx;
+}
+
+template <int NB, int XR, int NT>
+__device__ __forceinline__ void load_slice(const Weights<NB>& p, const Acts<XR, NT>& in, int s, u32x4 (&w)[NB],
+                                           u32x4 (&x)[x_loads(XR, NT)]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < in.nx) v[j] = *reinterpret_cast<const u32x4*>(in.x[j] + 128 * sl);
-    };
-    if (s0 < s1) load_x(s0, x[0]);
-    if (s0 + 1 < s1) load_x(s0 + 1, x[1]);
+    for (int b = 0; b < NB; ++b) w[b] = load16(p.w + 64 * s, p.wo[b]);
+#pragma unroll
+    for (int j = 0; j < x_loads(XR, NT); ++j)
+        if (brings<XR>(j, in.nx)) x[j] = load16(in.x + 256 * s, in.xo[j]);
+}
+
+template <int NB, int XR, int NT, int D>
+__device__ __forceinline__ void load_ahead(const Weights<NB>& p, const Acts<XR, NT>& in, int s0, int s1,
+                                           Ahead<NB, XR, NT, D>& a) {
+    if (s0 >= s1) return;
+    load_scales<NB>(p, s0, s1, a.sc);
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+        if (s0 + u < s1) load_slice<NB, XR, NT>(p, in, s0 + u, a.w[u], a.x[u]);
+}
+
+// acc[b] = the product over the 128-wide slices [s0, s1) of K, on top of acc.
+template <int NB, int XR, int NT, int D>
+__device__ __forceinline__ void mma_slices(Stage<NB, XR, NT>& st, const Weights<NB>& p, Ahead<NB, XR, NT, D>& a,
+                                           const Acts<XR, NT>& in, int s0, int s1, f32x4 (&acc)[NB]) {
+    static_assert(8 % D == 0, "a group of 8 slices' scales is whole rounds of requests");
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     for (int g = s0; g < s1; g += 8) {
 #pragma unroll
         for (int i = 0; i < 2 * NB; ++i) st.sc[lane + 64 * i] = a.sc[i];
         if (g + 8 < s1) load_scales<NB>(p, g + 8, s1, a.sc);
-        for (int h = g; h < min(g + 8, s1); h += kAhead) {
+        for (int h = g; h < min(g + 8, s1); h += D) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < D; ++u) {
                 const int s = h + u;
                 if (s >= s1) break;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) st.w[b][lane] = a.w[u][b];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < in.nx) st.x[64 * j + 16 * q + (m ^ (4 * j + q))] = x[u & 1][j];
-                if (s + kAhead < s1) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        a.w[u][b] = *reinterpret_cast<const u32x4*>(p.w[b] + 64 * (s + kAhead));
+                for (int j = 0; j < x_loads(XR, NT); ++j) {
+                    // fewer than four staged rows: lanes of the same row store the same
+                    const int r = (4 * j + q) % (XR * NT);
+                    if (brings<XR>(j, in.nx)) st.x[16 * r + (m ^ (r % XR))] = a.x[u][j];
                 }
-                if (s + 2 < s1) load_x(s + 2, x[u & 1]);
+                if (s + D < s1) load_slice<NB, XR, NT>(p, in, s + D, a.w[u], a.x[u]);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                u32x4 wf[NB], xf[4];
+                u32x4 wf[NB], xf[NT][4];
                 float sc[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     wf[b] = st.w[b][4 * m + ((q + (m >> 2)) & 3)];
                     sc[b] = e8m0_scale(reinterpret_cast<const uint8_t*>(st.sc)[((16 * b + m) * 8 + (s - g)) * 4 + q]);
                 }
+                const int r = m & (XR - 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xf[i] = st.x[16 * m + ((4 * q + i) ^ m)];
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) xf[n][i] = st.x[16 * (XR * n + r) + ((4 * q + i) ^ r)];
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4_to_bf16(wf[b][i], sc[b]),
-                                                                         __builtin_bit_cast(bf16x8, xf[i]), acc[b], 0,
-                                                                         0, 0);
+                    for (int b = 0; b < NB; ++b) {
+                        const bf16x8 wv = fp4_to_bf16(wf[b][i], sc[b]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, xf[n][i]),
+                                                                             acc[b], 0, 0, 0);
+                    }
             }
         }
     }
 }
 
 // Rows rows[n0 .. n) of a list as a wave's activations: row r reads line
-// r / div of x [.][K].
-__device__ __forceinline__ Acts acts_at(const uint16_t* x, const uint16_t* rows, int n0, int n, int div, int K) {
+// r / div of x [.][NT][K].
+template <int XR, int NT>
+__device__ __forceinline__ Acts<XR, NT> acts_at(const uint16_t* x, const uint16_t* rows, int n0, int n, int div,
+                                                int K) {
     const int lane = threadIdx.x & 63;
-    Acts in;
-    in.nx = min(4, (n - n0 + 3) / 4);
+    Acts<XR, NT> in;
+    in.x = reinterpret_cast<const uint8_t*>(x);
+    in.nx = min(XR / 4, (n - n0 + 3) / 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        in.x[j] = x + (size_t)(rows[min(n0 + 4 * j + (lane >> 4), n - 1)] / div) * K + 8 * (lane & 15);
+    for (int j = 0; j < XR / 4; ++j) {
+        const uint32_t line = (uint32_t)(rows[min(n0 + 4 * j + (lane >> 4), n - 1)] / div);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            in.xo[t * (XR / 4) + j] = (line * NT + t) * (uint32_t)(2 * K) + 16 * (lane & 15);
+    }
     return in;
 }
 
-// Two blocks of 16 weight rows (row0) times the group's rows, the waves of the
-// workgroup taking the quarters of K: the quarters' sums of rows n0 .. + 16,
-// added in order, to store(routed row, block 0, block 1) on wave 0's lanes.
-template <typename Store>
-__device__ __forceinline__ void group_product(GroupRows& s_g, Stage<2>* stage, const uint8_t* w, const uint8_t* s,
-                                              const size_t (&row0)[2], const uint16_t* x, int n, int div, int K,
+// NB blocks of 16 of the expert's weight rows (row0), and NP - 1 times the next
+// 16 NB rows, times the group's rows, XR at a time, the waves of the workgroup
+// taking the quarters of K.  Each wave then calls store(pass, routed row, sum),
+// sum(b) being block b's product with this lane's column (the quarters added in
+// order), on the columns that hold a row.  The next product's first loads are
+// in flight while one is reduced and stored.
+template <int NB, int XR, int NT, int D, int NP, typename Store>
+__device__ __forceinline__ void group_product(GroupRows& s_g, Stage<NB, XR, NT>* stage, const uint8_t* w,
+                                              const uint8_t* s,
+                                              const int (&row0)[NB], const uint16_t* x, int n, int div, int K,
                                               Store store) {
     const int lane = threadIdx.x & 63, wave = wave_index(), m = lane & 15;
     const int ns = K / 128, sl0 = wave * ns / 4, sl1 = (wave + 1) * ns / 4;
-    const Weights<2> p = weights_at<2>(w, s, row0, K);
-    for (int n0 = 0; n0 < n; n0 += 16) {
-        Ahead<2> a;
-        load_ahead<2>(p, sl0, sl1, a);
-        const Acts in = acts_at(x, s_g.rows, n0, n, div, K);
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        mma_slices<2>(stage[wave], p, a, in, sl0, sl1, acc);
-        f32x4* red = reinterpret_cast<f32x4*>(stage[wave].x);
-        red[lane] = acc[0];
-        red[64 + lane] = acc[1];
-        __syncthreads();
-        if (wave == 0 && n0 + m < n) {
-            f32x4 v[2];
+    Weights<NB> p = weights_at<NB>(w, s, row0, K);
+    Acts<XR, NT> in = acts_at<XR, NT>(x, s_g.rows, 0, n, div, K);
+    Ahead<NB, XR, NT, D> a;
+    load_ahead<NB, XR, NT, D>(p, in, sl0, sl1, a);
+    for (int pass = 0, n0 = 0; pass < NP;) {
+        f32x4 acc[NB];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                auto part = [&](int i) { return reinterpret_cast<const f32x4*>(stage[i].x)[64 * b + lane]; };
-                v[b] = ((part(0) + part(1)) + part(2)) + part(3);
-            }
-            store((int)s_g.rows[n0 + m], v[0], v[1]);
+        for (int b = 0; b < NB; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        mma_slices<NB, XR, NT, D>(stage[wave], p, a, in, sl0, sl1, acc);
+        const int done = pass, r0 = n0;
+        n0 += XR;
+        if (n0 >= n) {
+            n0 = 0;
+            ++pass;
+            p.w += (size_t)8 * NB * K;
+            p.s += (size_t)(NB / 2) * K;
         }
-        if (n0 + 16 < n) __syncthreads();   // the stages are written again
+        if (pass < NP) {
+            if (n > XR) in = acts_at<XR, NT>(x, s_g.rows, n0, n, div, K);
+            load_ahead<NB, XR, NT, D>(p, in, sl0, sl1, a);
+        }
+        f32x4* red = reinterpret_cast<f32x4*>(stage[wave].w);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) red[64 * b + lane] = acc[b];
+        __syncthreads();
+        if (m < XR && r0 + m < n) {
+            store(done, (int)s_g.rows[r0 + m], [&](int b) {
+                auto part = [&](int i) { return reinterpret_cast<const f32x4*>(stage[i].w)[64 * b + lane]; };
+                return ((part(0) + part(1)) + part(2)) + part(3);
+            });
+        }
+        if (pass < NP) __syncthreads();   // the stages are written again
     }
 }
 
 }  // namespace
 
-// Gate and up projections: workgroup = (group, 16 hidden units);
-// h[r] = silu(a) b as bfloat16.
+// Gate and up projections: workgroup = (group, 8 NB hidden units), half of its
+// weight rows the gate's, half the up's; h[r] = silu(a) b as two terms.
+template <int NB, int XR, int D>
 __global__ __launch_bounds__(256) void decode_up_kernel(const uint16_t* __restrict__ x,
                                                         const int32_t* __restrict__ idx,
                                                         const uint8_t* __restrict__ w1,
                                                         const uint8_t* __restrict__ s1, uint16_t* __restrict__ h,
                                                         int R, int E, int k, int d, int H) {
     __shared__ GroupRows s_g;
-    __shared__ Stage<2> stage[4];
-    const int nb = H / 16, g = blockIdx.x / nb, hb = blockIdx.x - g * nb;
+    __shared__ Stage<NB, XR, 1> stage[4];
+    const int nb = H / (8 * NB), g = blockIdx.x / nb, hb = blockIdx.x - g * nb;
     int e;
     const int n = group_rows(idx, R, E, g, e, s_g);
     if (n == 0) return;
-    // packed rows of hidden units 16 hb .. + 16: gate at 64 (hb / 2) + 16 (hb % 2), up 32 further
-    const size_t row = (size_t)e * 2 * H + 64 * (hb >> 1) + 16 * (hb & 1);
-    const int q = (threadIdx.x & 63) >> 4;
-    group_product(s_g, stage, w1, s1, {row, row + 32}, x, n, k, d, [&](int r, const f32x4& a, const f32x4& b) {
-        float o[4];
+    // packed rows of hidden unit u: gate at 64 (u / 32) + u % 32, up 32 further
+    const int u0 = 8 * NB * hb, wave = wave_index(), q = (threadIdx.x & 63) >> 4;
+    int row0[NB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-        *reinterpret_cast<uint2*>(h + (size_t)r * H + 16 * hb + 4 * q) =
-            make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    for (int b = 0; b < NB; ++b) row0[b] = 64 * (u0 / 32) + u0 % 32 + 16 * (b % (NB / 2)) + 32 * (b / (NB / 2));
+    group_product<NB, XR, 1, D, 1>(s_g, stage, w1 + (size_t)e * H * d, s1 + (size_t)e * H * (d / 16), row0, x, n, k, d,
+                                   [&](int, int r, auto sum) {
+        if (wave >= NB / 2) return;   // wave b: hidden units u0 + 16 b .. + 16
+        const f32x4 a = sum(wave), b = sum(wave + NB / 2);
+        float o[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
+            lo[i] = o[i] - bf16_round(o[i]);
+        }
+        uint16_t* dst = h + (size_t)r * 2 * H + u0 + 16 * wave + 4 * q;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        *reinterpret_cast<uint2*>(dst + H) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
     });
 }
 
-// Down projection: workgroup = (group, 32 outputs), ye[r][d] in float32.
+// Down projection: workgroup = (group, NP times 16 NB outputs), ye[r][d] in float32.
+template <int NB, int XR, int D, int NP>
 __global__ __launch_bounds__(256) void decode_down_kernel(const uint16_t* __restrict__ h,
                                                           const int32_t* __restrict__ idx,
                                                           const uint8_t* __restrict__ w2,
                                                           const uint8_t* __restrict__ s2, float* __restrict__ ye,
                                                           int R, int E, int d, int H) {
     __shared__ GroupRows s_g;
-    __shared__ Stage<2> stage[4];
-    const int nb = d / 32, g = blockIdx.x / nb, cb = blockIdx.x - g * nb;
+    __shared__ Stage<NB, XR, 2> stage[4];
+    const int nb = d / (16 * NB * NP), g = blockIdx.x / nb, cb = blockIdx.x - g * nb;
     int e;
     const int n = group_rows(idx, R, E, g, e, s_g);
     if (n == 0) return;
-    const size_t row = (size_t)e * d + 32 * cb;
-    const int q = (threadIdx.x & 63) >> 4;
-    group_product(s_g, stage, w2, s2, {row, row + 16}, h, n, 1, H, [&](int r, const f32x4& a, const f32x4& b) {
-        float* dst = ye + (size_t)r * d + 32 * cb + 4 * q;
-        *reinterpret_cast<f32x4*>(dst) = a;
-        *reinterpret_cast<f32x4*>(dst + 16) = b;
+    const int c0 = 16 * NB * NP * cb, wave = wave_index(), q = (threadIdx.x & 63) >> 4;
+    int row0[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) row0[b] = c0 + 16 * b;
+    group_product<NB, XR, 2, D, NP>(s_g, stage, w2 + (size_t)e * d * (H / 2), s2 + (size_t)e * d * (H / 32), row0, h, n, 1, H,
+                             [&](int pass, int r, auto sum) {
+        if (wave < NB) *reinterpret_cast<f32x4*>(ye + (size_t)r * d + c0 + 16 * (NB * pass + wave) + 4 * q) = sum(wave);
     });
 }
 
@@ -349,44 +426,57 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(const float* __rest
     *reinterpret_cast<uint2*>(y + (size_t)t * d + c) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
 }
 
-// Down projection and combine of few rows: workgroup = (token, 16 outputs),
-// sixteen waves, a wave per quarter of a slot in turn (the slot's h the only
+// Down projection and combine of few rows: workgroup = (token, 16 NB outputs),
+// sixteen waves, a wave per quarter of a slot in turn (the slot's h in every
 // column).  No float32 rows and no third launch, but tokens that share an
 // expert each read its weights.
+template <int NB, int D>
 __global__ __launch_bounds__(1024) void decode_down_token_kernel(const uint16_t* __restrict__ h,
                                                                  const int32_t* __restrict__ idx,
                                                                  const float* __restrict__ gate,
                                                                  const uint8_t* __restrict__ w2,
                                                                  const uint8_t* __restrict__ s2,
                                                                  uint16_t* __restrict__ y, int E, int k, int d, int H) {
-    __shared__ Stage<1> stage[16];
-    __shared__ float red[kMaxTopK][4][16];
+    __shared__ Stage<NB, 1, 2> stage[16];
+    __shared__ float red[kMaxTopK][4][16 * NB];
     __shared__ float s_gate[kMaxTopK];
     const int lane = threadIdx.x & 63, wave = wave_index(), m = lane & 15, q = lane >> 4;
-    const int nb = d / 16, t = blockIdx.x / nb, cb = blockIdx.x - t * nb;
-    const int ns = H / 128;
-    for (int u = wave; u < 4 * k; u += 16) {
-        const int j = u >> 2, quarter = u & 3, r = t * k + j, e = uniform(idx[r]);
-        const bool used = e >= 0 && e < E;
-        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-        if (used) {
-            const int sl0 = quarter * ns / 4, sl1 = (quarter + 1) * ns / 4;
-            const Weights<1> p = weights_at<1>(w2, s2, {(size_t)e * d + 16 * cb}, H);
-            Ahead<1> a;
-            load_ahead<1>(p, sl0, sl1, a);
-            const uint16_t* hr = h + (size_t)r * H + 8 * m;
-            mma_slices<1>(stage[wave], p, a, {{hr, hr, hr, hr}, 1}, sl0, sl1, acc);
+    const int nb = d / (16 * NB), t = blockIdx.x / nb, cb = blockIdx.x - t * nb;
+    const int ns = H / 128, quarter = wave & 3, sl0 = quarter * ns / 4, sl1 = (quarter + 1) * ns / 4;
+    int row0[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) row0[b] = 16 * (NB * cb + b);
+    // slot j of this wave: its expert's weights and h requested, -1 if it is not in use
+    auto request = [&](int j, Weights<NB>& p, Acts<1, 2>& in, Ahead<NB, 1, 2, D>& a) {
+        const int e = uniform(idx[t * k + j]);
+        if (e < 0 || e >= E) return -1;
+        p = weights_at<NB>(w2 + (size_t)e * d * (H / 2), s2 + (size_t)e * d * (H / 32), row0, H);
+        in = {reinterpret_cast<const uint8_t*>(h), {(uint32_t)(2 * (t * k + j) + (q & 1)) * (uint32_t)(2 * H) + 16 * m}, 1};
+        load_ahead<NB, 1, 2, D>(p, in, sl0, sl1, a);
+        return e;
+    };
+    Weights<NB> p;
+    Acts<1, 2> in;
+    Ahead<NB, 1, 2, D> a;
+    for (int j = wave >> 2; j < k; j += 4) {
+        const int e = request(j, p, in, a);
+        f32x4 acc[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if (e >= 0) mma_slices<NB, 1, 2, D>(stage[wave], p, a, in, sl0, sl1, acc);
+        if (m == 0) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) *reinterpret_cast<f32x4*>(&red[j][quarter][16 * b + 4 * q]) = acc[b];
         }
-        if (m == 0) *reinterpret_cast<f32x4*>(&red[j][quarter][4 * q]) = acc[0];
-        if (lane == 0 && quarter == 0) s_gate[j] = used ? gate[r] : 0.f;
+        if (lane == 0 && quarter == 0) s_gate[j] = e >= 0 ? gate[t * k + j] : 0.f;
     }
     __syncthreads();
-    if (threadIdx.x < 16) {
+    if (threadIdx.x < 16 * NB) {
         const int c = threadIdx.x;
         float s = 0.f;
         for (int j = 0; j < k; ++j)
             s = fmaf(s_gate[j], ((red[j][0][c] + red[j][1][c]) + red[j][2][c]) + red[j][3][c], s);
-        y[(size_t)t * d + 16 * cb + c] = f32_to_bf16(s);
+        y[(size_t)t * d + 16 * NB * cb + c] = f32_to_bf16(s);
     }
 }
 
@@ -446,13 +536,25 @@ hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const fl
                                  const uint8_t* w2, const uint8_t* s1, const uint8_t* s2, uint16_t* h, float* ye,
                                  uint16_t* y, int T, int d, int E, int k, int H, hipStream_t s) {
     const int R = T * k, G = R <= E ? R : E;
-    hipLaunchKernelGGL(decode_up_kernel, dim3(G * (H / 16)), dim3(256), 0, s, x, idx, w1, s1, h, R, E, k, d, H);
+    const dim3 wg(256);
+    if (R <= E)
+        hipLaunchKernelGGL((decode_up_kernel<2, 4, 4>), dim3(G * (H / 16)), wg, 0, s, x, idx, w1, s1, h, R, E, k, d, H);
+    else
+        hipLaunchKernelGGL((decode_up_kernel<4, 16, 2>), dim3(G * (H / 32)), wg, 0, s, x, idx, w1, s1, h, R, E, k, d, H);
     if (2 * R <= E) {
-        hipLaunchKernelGGL(decode_down_token_kernel, dim3(T * (d / 16)), dim3(1024), 0, s, h, idx, gate, w2, s2, y, E, k,
-                           d, H);
+        if (T * (d / 32) >= 256)
+            hipLaunchKernelGGL((decode_down_token_kernel<2, 4>), dim3(T * (d / 32)), dim3(1024), 0, s, h, idx, gate, w2,
+                               s2, y, E, k, d, H);
+        else
+            hipLaunchKernelGGL((decode_down_token_kernel<1, 4>), dim3(T * (d / 16)), dim3(1024), 0, s, h, idx, gate, w2,
+                               s2, y, E, k, d, H);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(decode_down_kernel, dim3(G * (d / 32)), dim3(256), 0, s, h, idx, w2, s2, ye, R, E, d, H);
+    if (R <= E)
+        hipLaunchKernelGGL((decode_down_kernel<2, 4, 4, 1>), dim3(G * (d / 32)), wg, 0, s, h, idx, w2, s2, ye, R, E, d, H);
+    else
+        hipLaunchKernelGGL((decode_down_kernel<4, 16, 2, 2>), dim3(G * (d / 128)), wg, 0, s, h, idx, w2, s2, ye, R, E, d,
+                           H);
     const dim3 cg((d / 4 + 255) / 256, T), cb(256);
     if (k <= 4) hipLaunchKernelGGL(decode_combine_kernel<4>, cg, cb, 0, s, ye, idx, gate, y, E, k, d);
     else if (k <= 8) hipLaunchKernelGGL(decode_combine_kernel<8>, cg, cb, 0, s, ye, idx, gate, y, E, k, d);

@@ -264,7 +264,7 @@ hipError_t launch_router_dw(int act, const float* dL, const void* x, float* part
 
 hipError_t launch_pack_mxfp4(const void* w_gate, const void* w_up, const void* w_down, uint8_t* w1, uint8_t* w2,
                              uint8_t* s1, uint8_t* s2, int E, int d, int H, hipStream_t s);
-// T <= kDecodeTokens; h [T k][H] bfloat16 and ye [T k][d] float32 are scratch.
+// T <= kDecodeTokens; h [T k][2][H] bfloat16 and ye [T k][d] float32 are scratch.
 hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const float* gate, const uint8_t* w1,
                                  const uint8_t* w2, const uint8_t* s1, const uint8_t* s2, uint16_t* h, float* ye,
                                  uint16_t* y, int T, int d, int E, int k, int H, hipStream_t s);

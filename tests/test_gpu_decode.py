@@ -3,7 +3,8 @@ moe_decode_experts, moe_decode) against its float64 oracle (marked gpu).
 
 The oracle multiplies with the values the packed weights stand for; its error
 bound follows float32 sums of K terms (K half-steps of the magnitudes) and h
-stored in bfloat16 through the block, and y itself is rounded once (2^-8)."""
+stored as two bfloat16 terms (2^-8 of 2^-8 of it left out) through the block,
+and y itself is rounded once (2^-8)."""
 import numpy as np
 import pytest
 import torch

@@ -540,7 +540,7 @@ hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const fl
     if (R <= E)
         hipLaunchKernelGGL((decode_up_kernel<2, 4, 4>), dim3(G * (H / 16)), wg, 0, s, x, idx, w1, s1, h, R, E, k, d, H);
     else
-        hipLaunchKernelGGL((decode_up_kernel<4, 16, 2>), dim3(G * (H / 32)), wg, 0, s, x, idx, w1, s1, h, R, E, k, d, H);
+        hipLaunchKernelGGL((decode_up_kernel<4, 16, 1>), dim3(G * (H / 32)), wg, 0, s, x, idx, w1, s1, h, R, E, k, d, H);
     if (2 * R <= E) {
         if (T * (d / 32) >= 256)
             hipLaunchKernelGGL((decode_down_token_kernel<2, 4>), dim3(T * (d / 32)), dim3(1024), 0, s, h, idx, gate, w2,
@@ -553,7 +553,7 @@ hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const fl
     if (R <= E)
         hipLaunchKernelGGL((decode_down_kernel<2, 4, 4, 1>), dim3(G * (d / 32)), wg, 0, s, h, idx, w2, s2, ye, R, E, d, H);
     else
-        hipLaunchKernelGGL((decode_down_kernel<4, 16, 2, 2>), dim3(G * (d / 128)), wg, 0, s, h, idx, w2, s2, ye, R, E, d,
+        hipLaunchKernelGGL((decode_down_kernel<4, 16, 1, 2>), dim3(G * (d / 128)), wg, 0, s, h, idx, w2, s2, ye, R, E, d,
                            H);
     const dim3 cg((d / 4 + 255) / 256, T), cb(256);
     if (k <= 4) hipLaunchKernelGGL(decode_combine_kernel<4>, cg, cb, 0, s, ye, idx, gate, y, E, k, d);

@@ -81,16 +81,16 @@ __device__ __forceinline__ void load_terms(const void* p, size_t i, int n, bool 
 
 // dx: a workgroup owns 64 tokens and 256 columns, a wave 64 of the columns.
 // D = W_r dL^T as 16 x 16 blocks: M = columns, N = tokens, K = experts.  Row m
-// of the wave's block mt is column 16 (m / 4) + 4 mt + m % 4, so that a lane's
-// four blocks hold 16 consecutive columns of one token and the result is read
-// and written in 16-byte pieces.  `add`: row t of add (pos NULL), or the sum
+// of the wave's block mt is column 32 (mt / 2) + 8 (m / 4) + 4 (mt % 2) + m % 4,
+// so that a lane's blocks 2 p and 2 p + 1 hold 8 consecutive columns of one
+// token and four lanes 32: the result is read and written in 64-byte pieces.  `add`: row t of add (pos NULL), or the sum
 // of its rows pos[t][0 .. k), or nothing (add NULL).
 template <bool BF>
 __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict__ dL, const void* __restrict__ w,
                                                         const void* add, const int32_t* __restrict__ pos, int k,
                                                         void* dx, int T, int d, int E) {
     constexpr int TA = BF ? 1 : 3;
-    constexpr int NC = BF ? 2 : 4;       // 16-byte chunks of 16 columns
+    constexpr int NC = BF ? 1 : 2;       // 16-byte chunks of 8 columns
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
     const int ncb = (d + 255) / 256, tb = blockIdx.x / ncb;
     const int t0 = tb * 64, c0 = (int)(blockIdx.x - tb * ncb) * 256 + wave * 64;
@@ -110,53 +110,59 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             bf16x8 a[TA];
-            load_terms<BF>(w, (size_t)(c0 + 16 * (m >> 2) + 4 * mt + (m & 3)) * E + e, n, vec, a);
+            load_terms<BF>(w, (size_t)(c0 + 32 * (mt >> 1) + 8 * (m >> 2) + 4 * (mt & 1) + (m & 3)) * E + e, n, vec, a);
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) acc[mt][nt] = mfma_terms<TA>(a, b[nt], acc[mt][nt]);
         }
     }
-    const size_t row_chunks = (size_t)d / (BF ? 8 : 4), cb = (size_t)(c0 + 16 * q) / (BF ? 8 : 4);
+    // 8 columns from c0 + 32 p + 8 q: NC chunks
+    const size_t row_chunks = (size_t)d / (BF ? 8 : 4), cb = (size_t)(c0 + 8 * q) / (BF ? 8 : 4);
     const u32x4* src = static_cast<const u32x4*>(add);
     u32x4* dst = static_cast<u32x4*>(dx);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         const int t = t0 + 16 * nt + m;
         if (t >= T) continue;
-        float base[16];
+        float base[2][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) base[i] = 0.f;
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) base[p][i] = 0.f;
         if (src) {
             const int rows = pos ? k : 1;
             for (int j = 0; j < rows; ++j) {
                 const size_t r = pos ? (size_t)pos[(size_t)t * k + j] : (size_t)t;
 #pragma unroll
-                for (int g = 0; g < NC; ++g) {
-                    const u32x4 v = src[r * row_chunks + cb + g];
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (BF) {
-                            base[8 * g + 2 * i] += __uint_as_float(v[i] << 16);
-                            base[8 * g + 2 * i + 1] += __uint_as_float(v[i] & 0xFFFF0000u);
-                        } else {
-                            base[4 * g + i] += __uint_as_float(v[i]);
+                    for (int g = 0; g < NC; ++g) {
+                        const u32x4 v = src[r * row_chunks + cb + 4 * NC * p + g];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (BF) {
+                                base[p][2 * i] += __uint_as_float(v[i] << 16);
+                                base[p][2 * i + 1] += __uint_as_float(v[i] & 0xFFFF0000u);
+                            } else {
+                                base[p][4 * (g % 2) + i] += __uint_as_float(v[i]);
+                            }
                         }
                     }
-                }
             }
         }
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) base[4 * mt + i] += acc[mt][nt][i];
+            for (int i = 0; i < 4; ++i) base[mt >> 1][4 * (mt & 1) + i] += acc[mt][nt][i];
 #pragma unroll
-        for (int g = 0; g < NC; ++g) {
-            u32x4 o;
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = BF ? pack_bf16x2(base[(8 * g + 2 * i) & 15], base[(8 * g + 2 * i + 1) & 15])
-                          : __float_as_uint(base[(4 * g + i) & 15]);
-            dst[(size_t)t * row_chunks + cb + g] = o;
-        }
+            for (int g = 0; g < NC; ++g) {
+                u32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = BF ? pack_bf16x2(base[p][2 * i], base[p][2 * i + 1]) : __float_as_uint(base[p][4 * (g % 2) + i]);
+                dst[(size_t)t * row_chunks + cb + 4 * NC * p + g] = o;
+            }
     }
 }
 

@@ -207,7 +207,7 @@ bool off_by(const void* ptr, size_t align) { return (reinterpret_cast<uintptr_t>
 // dense router weight gradient.
 size_t bwd_aux_bytes(const moe_problem& p) {
     const bool learned = !(p.flags & MOE_LOGITS_GIVEN);
-    return bwd_layout(p).total + (learned ? align256(router_dw_part_bytes(p.T, p.d_model, p.n_experts)) : 0);
+    return bwd_layout(p).total + (learned ? align256(router_dw_part_bytes(p.act_dtype, p.T, p.d_model, p.n_experts)) : 0);
 }
 
 // Balance loss: float sums [blocks][E] and [blocks], then int counts likewise.
@@ -1012,7 +1012,7 @@ int32_t moe_router_backward_workspace_bytes(const moe_problem* p, size_t* bytes)
     int32_t st = check_problem(p);
     if (st) return st;
     if (!bytes) return MOE_ERR_NULL;
-    *bytes = align256(router_dw_part_bytes(p->T, p->d_model, p->n_experts));
+    *bytes = align256(router_dw_part_bytes(p->act_dtype, p->T, p->d_model, p->n_experts));
     return MOE_OK;
 }
 
@@ -1020,7 +1020,7 @@ int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const vo
                             const void* dx_in, void* dx, float* dw_router, void* ws, size_t ws_bytes, void* stream) {
     int32_t st = check_problem(p);
     if (st) return st;
-    const size_t need = align256(router_dw_part_bytes(p->T, p->d_model, p->n_experts));
+    const size_t need = align256(router_dw_part_bytes(p->act_dtype, p->T, p->d_model, p->n_experts));
     if (!dlogits || !x || !w_router || !dx || !dw_router || (need && !ws)) return MOE_ERR_NULL;
     if (off_by(dlogits, 16) || off_by(x, 16) || off_by(w_router, 16) || off_by(dx_in, 16) || off_by(dx, 16) ||
         off_by(dw_router, 16) || off_by(ws, 16) || dx == x)

@@ -256,7 +256,7 @@ hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const in
 hipError_t launch_router_dx(int act, const float* dL, const void* w_router, const void* add, const int32_t* pos, int k,
                             void* dx, int T, int d, int E, hipStream_t s);
 // dw_router = x^T dL; part: router_dw_part_bytes (may be 0) of scratch.
-size_t router_dw_part_bytes(int T, int d, int E);
+size_t router_dw_part_bytes(int act, int T, int d, int E);
 hipError_t launch_router_dw(int act, const float* dL, const void* x, float* part, float* dw_router, int T, int d,
                             int E, hipStream_t s);
 

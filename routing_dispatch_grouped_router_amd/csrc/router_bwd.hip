@@ -19,26 +19,32 @@ namespace moe {
 
 namespace {
 
-// Three bfloat16 terms of eight float32 values.
+// Three bfloat16 terms of eight float32 values, two at a time.
 __device__ __forceinline__ void split3(const float (&v)[8], bf16x8 (&o)[3]) {
+    u32x4 w[3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __bf16 a = (__bf16)v[i];
-        const float r = v[i] - (float)a;
-        const __bf16 b = (__bf16)r;
-        o[0][i] = a;
-        o[1][i] = b;
-        o[2][i] = (__bf16)(r - (float)b);
+    for (int i = 0; i < 4; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint32_t u = pack_bf16x2(a, b);
+            w[p][i] = u;
+            a -= __uint_as_float(u << 16);
+            b -= __uint_as_float(u & 0xFFFF0000u);
+        }
     }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) o[p] = __builtin_bit_cast(bf16x8, w[p]);
 }
 
-// c += a b for operands of TA and three terms.
-template <int TA>
-__device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[TA], const bf16x8 (&b)[3], f32x4 c) {
+// c += a b for operands of TA and TB terms (1 or 3), the smallest products first.
+template <int TA, int TB>
+__device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[TA], const bf16x8 (&b)[TB], f32x4 c) {
 #pragma unroll
-    for (int i = TA - 1; i >= 0; --i)
+    for (int n = 2; n >= 0; --n)
 #pragma unroll
-        for (int j = 2 - i; j >= 0; --j) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], c, 0, 0, 0);
+        for (int i = 0; i <= n; ++i)
+            if (i < TA && n - i < TB) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[n - i], c, 0, 0, 0);
     return c;
 }
 
@@ -79,102 +85,149 @@ __device__ __forceinline__ void load_terms(const void* p, size_t i, int n, bool 
 
 }  // namespace
 
-// dx: a workgroup owns 64 tokens and 256 columns, a wave 64 of the columns.
-// D = W_r dL^T as 16 x 16 blocks: M = columns, N = tokens, K = experts.  Row m
-// of the wave's block mt is column 32 (mt / 2) + 8 (m / 4) + 4 (mt % 2) + m % 4,
-// so that a lane's blocks 2 p and 2 p + 1 hold 8 consecutive columns of one
-// token and four lanes 32: the result is read and written in 64-byte pieces.  `add`: row t of add (pos NULL), or the sum
-// of its rows pos[t][0 .. k), or nothing (add NULL).
+// dx: a workgroup owns 64 tokens and 256 columns, a wave 32 by 128 of them, as
+// 16 x 16 blocks: M = tokens, N = columns, K = experts.  Column n of the wave's
+// block j is column 8 n + j, so that a lane's eight blocks hold 8 consecutive
+// columns of a token and sixteen lanes 128: add is read and dx written in whole
+// lines (a lane layout with a row per lane cost the memory pipe an access per
+// lane, 126 us at T = 16384, d = 4096, E = 64).  Both operands pass through LDS
+// in fragment order, 32 experts at a time, loaded in whole 64- and 128-byte
+// pieces and split once for the workgroup; two buffers, the next experts' loads
+// in flight during a step's products.  `add`: row t of add (pos NULL; requested
+// before the products), or the sum of its rows pos[t][0 .. k), or nothing (NULL).
 template <bool BF>
 __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict__ dL, const void* __restrict__ w,
                                                         const void* add, const int32_t* __restrict__ pos, int k,
                                                         void* dx, int T, int d, int E) {
     constexpr int TA = BF ? 1 : 3;
-    constexpr int NC = BF ? 1 : 2;       // 16-byte chunks of 8 columns
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
+    constexpr int NC = BF ? 1 : 2;           // 16-byte chunks of 8 columns
+    __shared__ u32x4 s_a[2][4][3][64];       // dL: [token block][term], lane (token m, experts 8 q ..) at 16 q + (m ^ 4 q)
+    __shared__ u32x4 s_w[2][16][TA][64];     // W_r: [block][term], lane (column n, experts 8 q ..) at 16 q + (n ^ 4 q ^ j % 4)
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
     const int ncb = (d + 255) / 256, tb = blockIdx.x / ncb;
-    const int t0 = tb * 64, c0 = (int)(blockIdx.x - tb * ncb) * 256 + wave * 64;
-    if (c0 >= d) return;
+    const int t0 = tb * 64, c0 = (int)(blockIdx.x - tb * ncb) * 256;
+    const int wt = t0 + 32 * (wave & 1), wc = c0 + 128 * (wave >> 1);
     const bool vec = (E & 7) == 0;
-    f32x4 acc[4][4];   // [column block][token block]
+    const size_t row_chunks = (size_t)d / (BF ? 8 : 4), cb = (size_t)(wc + 8 * m) / (BF ? 8 : 4);
+    const bool in_cols = wc + 8 * m < d;
+    const u32x4* src = static_cast<const u32x4*>(add);
+
+    // thread: experts 8 (tid % 4) .. of token tid / 4 and of columns tid / 4 + 64 i
+    const int lr = tid >> 2, lq = tid & 3;
+    bf16x8 ra[3], rw[4][TA];
+    auto load = [&](int e0) {
+        const int e = e0 + 8 * lq, n = E - e;
+        load_terms<false>(dL, (size_t)min(t0 + lr, T - 1) * E + e, n, vec, ra);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) load_terms<BF>(w, (size_t)min(c0 + lr + 64 * i, d - 1) * E + e, n, vec, rw[i]);
+    };
+    auto stage = [&](int buf) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + 8 * q, n = E - e;
-        bf16x8 b[4][3];
+        for (int p = 0; p < 3; ++p)
+            s_a[buf][lr >> 4][p][16 * lq + ((lr & 15) ^ (4 * lq))] = __builtin_bit_cast(u32x4, ra[p]);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-            load_terms<false>(dL, (size_t)min(t0 + 16 * nt + m, T - 1) * E + e, n, vec, b[nt]);
+        for (int i = 0; i < 4; ++i) {
+            const int c = lr + 64 * i, j = c & 7, n = (c >> 3) & 15;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            bf16x8 a[TA];
-            load_terms<BF>(w, (size_t)(c0 + 32 * (mt >> 1) + 8 * (m >> 2) + 4 * (mt & 1) + (m & 3)) * E + e, n, vec, a);
+            for (int p = 0; p < TA; ++p)
+                s_w[buf][8 * (c >> 7) + j][p][16 * lq + (n ^ (4 * lq) ^ (j & 3))] = __builtin_bit_cast(u32x4, rw[i][p]);
+        }
+    };
+    load(0);
+    u32x4 base[2][4][NC];
+    if (src && !pos) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) acc[mt][nt] = mfma_terms<TA>(a, b[nt], acc[mt][nt]);
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = min(wt + 16 * mt + 4 * q + i, T - 1);
+#pragma unroll
+                for (int g = 0; g < NC; ++g) base[mt][i][g] = in_cols ? src[t * row_chunks + cb + g] : (u32x4){0u, 0u, 0u, 0u};
+            }
+    }
+    f32x4 acc[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    int buf = 0;
+    for (int e0 = 0; e0 < E; e0 += 32, buf ^= 1) {
+        stage(buf);
+        __syncthreads();   // also: every wave has left the buffer that is written next
+        if (e0 + 32 < E) load(e0 + 32);
+        bf16x8 a[2][3];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                a[mt][p] = __builtin_bit_cast(bf16x8, s_a[buf][2 * (wave & 1) + mt][p][16 * q + (m ^ (4 * q))]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            bf16x8 b[TA];
+#pragma unroll
+            for (int p = 0; p < TA; ++p)
+                b[p] = __builtin_bit_cast(bf16x8, s_w[buf][8 * (wave >> 1) + j][p][16 * q + (m ^ (4 * q) ^ (j & 3))]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) acc[mt][j] = mfma_terms<3, TA>(a[mt], b, acc[mt][j]);
         }
     }
-    // 8 columns from c0 + 32 p + 8 q: NC chunks
-    const size_t row_chunks = (size_t)d / (BF ? 8 : 4), cb = (size_t)(c0 + 8 * q) / (BF ? 8 : 4);
-    const u32x4* src = static_cast<const u32x4*>(add);
+    if (!in_cols) return;
     u32x4* dst = static_cast<u32x4*>(dx);
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        const int t = t0 + 16 * nt + m;
-        if (t >= T) continue;
-        float base[2][8];
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int i = 0; i < 4; ++i) {
+            const int t = wt + 16 * mt + 4 * q + i;
+            if (t >= T) continue;
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) base[p][i] = 0.f;
-        if (src) {
-            const int rows = pos ? k : 1;
-            for (int j = 0; j < rows; ++j) {
-                const size_t r = pos ? (size_t)pos[(size_t)t * k + j] : (size_t)t;
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            auto plus = [&](const u32x4& c, int g) {
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int g = 0; g < NC; ++g) {
-                        const u32x4 v = src[r * row_chunks + cb + 4 * NC * p + g];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (BF) {
-                                base[p][2 * i] += __uint_as_float(v[i] << 16);
-                                base[p][2 * i + 1] += __uint_as_float(v[i] & 0xFFFF0000u);
-                            } else {
-                                base[p][4 * (g % 2) + i] += __uint_as_float(v[i]);
-                            }
-                        }
+                for (int h = 0; h < 4; ++h) {
+                    if (BF) {
+                        v[2 * h] += __uint_as_float(c[h] << 16);
+                        v[2 * h + 1] += __uint_as_float(c[h] & 0xFFFF0000u);
+                    } else {
+                        v[4 * g + h] += __uint_as_float(c[h]);
                     }
+                }
+            };
+            if (pos) {
+                for (int s = 0; s < k; ++s) {
+                    const size_t r = (size_t)pos[(size_t)t * k + s];
+#pragma unroll
+                    for (int g = 0; g < NC; ++g) plus(src[r * row_chunks + cb + g], g);
+                }
+            } else if (src) {
+#pragma unroll
+                for (int g = 0; g < NC; ++g) plus(base[mt][i][g], g);
             }
-        }
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) base[mt >> 1][4 * (mt & 1) + i] += acc[mt][nt][i];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
+            for (int j = 0; j < 8; ++j) v[j] += acc[mt][j][i];
 #pragma unroll
             for (int g = 0; g < NC; ++g) {
                 u32x4 o;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = BF ? pack_bf16x2(base[p][2 * i], base[p][2 * i + 1]) : __float_as_uint(base[p][4 * (g % 2) + i]);
-                dst[(size_t)t * row_chunks + cb + 4 * NC * p + g] = o;
+                for (int h = 0; h < 4; ++h)
+                    o[h] = BF ? pack_bf16x2(v[2 * h], v[2 * h + 1]) : __float_as_uint(v[4 * g + h]);
+                dst[t * row_chunks + cb + g] = o;
             }
-    }
+        }
 }
 
-// dW_r partials: a workgroup sums 128 columns x 16 NT experts over a range of
+// dW_r partials: a workgroup sums CT columns x 16 NT experts over a range of
 // tokens, 32 at a time.  M = columns, N = experts, K = tokens.  The x tile is
 // staged in LDS as blocks of 16 columns [32 tokens][16] (32-byte rows, blocks
 // 32 bytes apart in the banks) and read transposed (ds_read_b64_tr_b16: 16
 // lanes addressing rows r0 + L / 4 and columns 4 (L % 4) .. + 3 receive rows
 // r0 .. r0 + 3 of column L); the dL operands are split once, by wave nt for
-// experts 16 nt .. + 16, and shared through LDS.  Two buffers: the next tile's
-// loads are in flight during a tile's products.
-template <bool BF, int NT>
+// experts 16 nt .. + 16, and shared through LDS.  LDS reads are the bound, and
+// a dL block is three times an x block, so with 64 experts two waves share the
+// columns and a wave's tile is 128 columns by 32 experts (32 by 64: 50 us at
+// T = 16384, d = 4096, E = 64).  Two buffers, and the loads of the next PD
+// tiles in flight.
+template <bool BF, int NT, int CT>
 __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict__ dL, const void* __restrict__ x,
                                                         float* __restrict__ part, int T, int d, int E, int rows) {
     typedef short v4s __attribute__((ext_vector_type(4)));
@@ -182,45 +235,59 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
     constexpr int TA = BF ? 1 : 3;
     constexpr int kTile = 32 * 32 + 32;                 // bytes of a 16-column block, padded
     constexpr int NX = BF ? 1 : 2;                      // 16-byte loads of 8 columns
-    __shared__ __align__(16) char s_x[2][TA][8 * kTile];
+    constexpr int PD = 2;
+    constexpr int XI = CT / 64;                         // 8-column items of a thread: 32 tokens x CT / 8 chunks
+    constexpr int WE = NT == 4 ? 2 : 1, WC = 4 / WE;    // waves over the experts, over the columns
+    constexpr int MT = CT / WC / 16, NW = NT / WE;      // a wave's blocks
+    __shared__ __align__(16) char s_x[2][TA][CT / 16 * kTile];
     __shared__ u32x4 s_b[2][NT][3][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
-    const int c0 = blockIdx.x * 128, e0 = blockIdx.y * 16 * NT;
+    const int c0 = blockIdx.x * CT, e0 = blockIdx.y * 16 * NT;
     const int t0 = blockIdx.z * rows, t1 = min(T, t0 + rows);
+    const int wm = MT * (wave % WC), wn = NW * (wave / WC);   // the wave's first blocks
     const size_t rowc = (size_t)d / (BF ? 8 : 4);       // 16-byte chunks of a row
-    f32x4 acc[2][NT];
+    const int lt = tid / (CT / 8), lc = tid % (CT / 8); // loader: token lt + 2048 / CT i, columns 8 lc .. + 8
+    f32x4 acc[MT][NW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NW; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    u32x4 xr[2][NX];
-    float br[8];
-    // thread item i: token tid / 16 + 16 i of the tile, columns 8 (tid % 16) .. + 8
-    auto load = [&](int tb) {
+    u32x4 xr[PD][XI][NX];
+    float br[PD][8];
+    // this thread's columns and expert, clamped (what is past d or E is not stored)
+    const uint32_t xc = (uint32_t)min(c0 + 8 * lc, d - 8) / (BF ? 8 : 4);
+    const int be = min(e0 + 16 * min(wave, NT - 1) + m, E - 1);
+    auto load = [&](int tb, u32x4 (&xr)[XI][NX], float (&br)[8]) {
+        const u32x4* xt = static_cast<const u32x4*>(x) + (size_t)tb * rowc;   // uniform, as are the rows' steps
+        const float* lb = dL + (size_t)tb * E;
+        if (tb + 32 <= t1) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = tb + (tid >> 4) + 16 * i, c = c0 + 8 * (tid & 15);
+            for (int i = 0; i < XI; ++i)
 #pragma unroll
-            for (int g = 0; g < NX; ++g)
-                xr[i][g] = t < t1 && c < d
-                               ? static_cast<const u32x4*>(x)[(size_t)t * rowc + (size_t)c / (BF ? 8 : 4) + g]
-                               : (u32x4){0u, 0u, 0u, 0u};
-        }
-        if (wave < NT) {
-            const int e = e0 + 16 * wave + m;
+                for (int g = 0; g < NX; ++g)
+                    xr[i][g] = (xt + 2048 / CT * i * rowc)[(uint32_t)(lt * rowc) + xc + g];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int t = tb + 8 * q + j;
-                br[j] = t < t1 && e < E ? dL[(size_t)t * E + e] : 0.f;
-            }
+            for (int j = 0; j < 8; ++j) br[j] = (lb + (size_t)j * E)[(uint32_t)(8 * q * E + be)];
+        } else {   // the last tile: rows clamped, and staged as zero
+            const int last = t1 - 1 - tb;
+#pragma unroll
+            for (int i = 0; i < XI; ++i)
+#pragma unroll
+                for (int g = 0; g < NX; ++g) xr[i][g] = xt[min(lt + 2048 / CT * i, last) * rowc + xc + g];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) br[j] = lb[(size_t)min(8 * q + j, last) * E + be];
         }
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](int buf, int tb, u32x4 (&xr)[XI][NX], float (&br)[8]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int tl = (tid >> 4) + 16 * i, c8 = tid & 15;
-            const int off = (c8 >> 1) * kTile + tl * 32 + (c8 & 1) * 16;
+        for (int i = 0; i < XI; ++i) {
+            const int tl = lt + 2048 / CT * i;
+            const int off = (lc >> 1) * kTile + tl * 32 + (lc & 1) * 16;
+            if (tb + 32 > t1) {
+#pragma unroll
+                for (int g = 0; g < NX; ++g) xr[i][g] = tb + tl < t1 ? xr[i][g] : (u32x4){0u, 0u, 0u, 0u};
+            }
             if constexpr (BF) {
                 *reinterpret_cast<u32x4*>(&s_x[buf][0][off]) = xr[i][0];
             } else {
@@ -235,50 +302,64 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
         }
         if (wave < NT) {
             bf16x8 o[3];
+            if (tb + 32 > t1) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) br[j] = tb + 8 * q + j < t1 ? br[j] : 0.f;
+            }
             split3(br, o);
 #pragma unroll
             for (int p = 0; p < 3; ++p) s_b[buf][wave][p][lane] = __builtin_bit_cast(u32x4, o[p]);
         }
     };
 
-    load(t0);
-    int buf = 0;
-    for (int tb = t0; tb < t1; tb += 32, buf ^= 1) {
-        stage(buf);
-        __syncthreads();   // also: every wave has left the buffer that is written next
-        if (tb + 32 < t1) load(tb + 32);
-        bf16x8 a[2][TA];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+    for (int u = 0; u < PD; ++u)
+        if (t0 + 32 * u < t1) load(t0 + 32 * u, xr[u], br[u]);
+    auto tile = [&](int tb, int u) {
+        const int buf = u & 1;
+        stage(buf, tb, xr[u], br[u]);
+        __syncthreads();   // also: every wave has left the buffer that is written next
+        if (tb + 32 * PD < t1) load(tb + 32 * PD, xr[u], br[u]);
+        bf16x8 b[NW][3];
+#pragma unroll
+        for (int nt = 0; nt < NW; ++nt)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) b[nt][p] = __builtin_bit_cast(bf16x8, s_b[buf][wn + nt][p][lane]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            bf16x8 a[TA];
 #pragma unroll
             for (int p = 0; p < TA; ++p) {
                 const __attribute__((address_space(3))) char* base =
                     (const __attribute__((address_space(3))) char*)(const __attribute__((address_space(3))) void*)
-                        &s_x[buf][p][(2 * wave + mt) * kTile];
+                        &s_x[buf][p][(wm + mt) * kTile];
                 const uint32_t off = (uint32_t)(8 * q + m / 4) * 32u + (uint32_t)(m % 4) * 8u;
                 const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(base + off));
                 const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(base + off + 128u));
-                a[mt][p] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                a[p] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            bf16x8 b[3];
-#pragma unroll
-            for (int p = 0; p < 3; ++p) b[p] = __builtin_bit_cast(bf16x8, s_b[buf][nt][p][lane]);
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) acc[mt][nt] = mfma_terms<TA>(a[mt], b, acc[mt][nt]);
+            for (int nt = 0; nt < NW; ++nt) acc[mt][nt] = mfma_terms<TA, 3>(a, b[nt], acc[mt][nt]);
         }
+    };
+    for (int tb = t0; tb < t1; tb += 32 * PD) {
+#pragma unroll
+        for (int u = 0; u < PD; ++u)
+            if (tb + 32 * u < t1) tile(tb + 32 * u, u);
     }
     float* dst = part + (size_t)blockIdx.z * d * E;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int nt = 0; nt < NW; ++nt) {
+        const int e = e0 + 16 * (wn + nt) + m;
+        if (e >= E) continue;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int mt = 0; mt < MT; ++mt) {
+            const int c = c0 + 16 * (wm + mt) + 4 * q;
+            if (c >= d) continue;   // d % 64 == 0: whole blocks
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = c0 + 32 * wave + 16 * mt + 4 * q + i, e = e0 + 16 * nt + m;
-                if (c < d && e < E) dst[(size_t)c * E + e] = acc[mt][nt][i];
-            }
+            for (int i = 0; i < 4; ++i) dst[(size_t)(c + i) * E + e] = acc[mt][nt][i];
+        }
+    }
 }
 
 // dw[i] = sum over the S token ranges of part[.][i], in order.
@@ -303,13 +384,14 @@ namespace {
 // Expert blocks per workgroup, and the tokens of a range: ranges so that about
 // two workgroups run on every compute unit, at least 128 tokens each.
 struct RouterDwPlan {
-    int nt, wx, wy, rows, S;
+    int nt, ct, wx, wy, rows, S;
 };
 
-RouterDwPlan router_dw_plan(int T, int d, int E) {
+RouterDwPlan router_dw_plan(int act, int T, int d, int E) {
     RouterDwPlan p{};
     p.nt = E <= 16 ? 1 : (E <= 32 ? 2 : 4);
-    p.wx = (d + 127) / 128;
+    p.ct = act == kF32 ? 128 : 256;   // three x terms take the LDS of a wider tile
+    p.wx = (d + p.ct - 1) / p.ct;
     p.wy = (E + 16 * p.nt - 1) / (16 * p.nt);
     const int want = std::max(1, 512 / (p.wx * p.wy));
     const int ranges = std::max(1, std::min(want, (T + 127) / 128));
@@ -321,10 +403,11 @@ RouterDwPlan router_dw_plan(int T, int d, int E) {
 template <bool BF>
 void launch_router_dw_t(const float* dL, const void* x, float* dst, const RouterDwPlan& p, int T, int d, int E,
                         hipStream_t s) {
+    constexpr int CT = BF ? 256 : 128;
     const dim3 g(p.wx, p.wy, p.S), b(256);
-    if (p.nt == 1) hipLaunchKernelGGL((router_dw_kernel<BF, 1>), g, b, 0, s, dL, x, dst, T, d, E, p.rows);
-    else if (p.nt == 2) hipLaunchKernelGGL((router_dw_kernel<BF, 2>), g, b, 0, s, dL, x, dst, T, d, E, p.rows);
-    else hipLaunchKernelGGL((router_dw_kernel<BF, 4>), g, b, 0, s, dL, x, dst, T, d, E, p.rows);
+    if (p.nt == 1) hipLaunchKernelGGL((router_dw_kernel<BF, 1, CT>), g, b, 0, s, dL, x, dst, T, d, E, p.rows);
+    else if (p.nt == 2) hipLaunchKernelGGL((router_dw_kernel<BF, 2, CT>), g, b, 0, s, dL, x, dst, T, d, E, p.rows);
+    else hipLaunchKernelGGL((router_dw_kernel<BF, 4, CT>), g, b, 0, s, dL, x, dst, T, d, E, p.rows);
 }
 
 }  // namespace
@@ -339,14 +422,14 @@ hipError_t launch_router_dx(int act, const float* dL, const void* w_router, cons
     return hipGetLastError();
 }
 
-size_t router_dw_part_bytes(int T, int d, int E) {
-    const RouterDwPlan p = router_dw_plan(T, d, E);
+size_t router_dw_part_bytes(int act, int T, int d, int E) {
+    const RouterDwPlan p = router_dw_plan(act, T, d, E);
     return p.S > 1 ? (size_t)p.S * d * E * 4 : 0;
 }
 
 hipError_t launch_router_dw(int act, const float* dL, const void* x, float* part, float* dw_router, int T, int d,
                             int E, hipStream_t s) {
-    const RouterDwPlan p = router_dw_plan(T, d, E);
+    const RouterDwPlan p = router_dw_plan(act, T, d, E);
     float* dst = p.S > 1 ? part : dw_router;   // one range: no partial sums
     if (act == kF32) launch_router_dw_t<false>(dL, x, dst, p, T, d, E, s);
     else launch_router_dw_t<true>(dL, x, dst, p, T, d, E, s);

@@ -518,8 +518,9 @@ int32_t moe_forward_quantized(const moe_problem* p, const void* x, const uint8_t
  *   dloss  : device float32 [2], the gradient for the two losses
  *   dlogits: device float32 [T, E] out
  *   ws     : device, moe_balance_workspace_bytes (host-only query)
- * Sums run in a fixed order (bitwise reproducible).  Errors: MOE_ERR_NULL,
- * MOE_ERR_WORKSPACE. */
+ * dlogits may be logits (in place).  logits, dlogits and ws are 16-byte
+ * aligned.  Sums run in a fixed order (bitwise reproducible).  Errors:
+ * MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an unaligned pointer. */
 int32_t moe_balance_workspace_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                          int32_t* counts, float* loss, void* ws, size_t ws_bytes, void* stream);

@@ -131,6 +131,11 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _own(t):
+    """Address of a buffer that the caller's object allocated itself (or None)."""
+    return None if t is None else t.data_ptr()
+
+
 # The handle of a device's current stream without making a Stream object of it
 # (0.1 instead of 2.9 us, of the 10 us that a small call took); not a documented
 # function, so the documented way stands in where it is missing.
@@ -487,8 +492,8 @@ class Norm:
             _expect(residual, shape, dt, "residual")
         _on_current(x)
         _check("moe_norm", lib().moe_norm(
-            self._p, _ptr(x), _ptr(residual), _ptr(weight), self.eps, _ptr(self.sum), _ptr(self.y),
-            _ptr(self.q), _ptr(self.q_scale), _ptr(self.rstd), _stream(stream)))
+            self._p, _ptr(x), _ptr(residual), _ptr(weight), self.eps, _own(self.sum), _own(self.y),
+            _own(self.q), _own(self.q_scale), _own(self.rstd), _stream(stream)))
         return self.y
 
 
@@ -514,8 +519,8 @@ class NormBackward:
             _expect(dsum, shape, dt, "dsum")
         _on_current(dy, "dy")
         _check("moe_norm_backward", lib().moe_norm_backward(
-            self._p, _ptr(dy), _ptr(dsum), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(self.ds),
-            _ptr(self.dweight), _ptr(self.ws), self.ws.numel(), _stream(stream)))
+            self._p, _ptr(dy), _ptr(dsum), _ptr(s), _ptr(weight), _ptr(rstd), _own(self.ds),
+            _own(self.dweight), _own(self.ws), self.ws.numel(), _stream(stream)))
         return dict(ds=self.ds, dweight=self.dweight)
 
 
@@ -543,8 +548,8 @@ class BalanceLoss:
         self._expect_logits(logits, mask)
         _expect(idx, self._choices, torch.int32, "idx")
         _check("moe_balance_loss", lib().moe_balance_loss(
-            self._p, _ptr(logits), _ptr(idx), _ptr(mask), _ptr(self.counts_live), _ptr(self.loss),
-            _ptr(self.ws), self.ws.numel(), _stream(stream)))
+            self._p, _ptr(logits), _ptr(idx), _ptr(mask), _own(self.counts_live), _own(self.loss),
+            _own(self.ws), self.ws.numel(), _stream(stream)))
         return self.loss
 
     def backward(self, logits, dloss, mask=None, stream=None):
@@ -552,7 +557,7 @@ class BalanceLoss:
         self._expect_logits(logits, mask)
         _expect(dloss, (2,), torch.float32, "dloss")
         _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-            self._p, _ptr(logits), _ptr(mask), _ptr(self.counts_live), _ptr(dloss), _ptr(self.dlogits),
+            self._p, _ptr(logits), _ptr(mask), _own(self.counts_live), _ptr(dloss), _own(self.dlogits),
             _stream(stream)))
         return self.dlogits
 
@@ -577,8 +582,8 @@ class RouterBackward:
             _expect(dx_in, shape, dt, "dx_in")
         _on_current(x)
         _check("moe_router_backward", lib().moe_router_backward(
-            self._p, _ptr(dlogits), _ptr(x), _ptr(w_router), _ptr(dx_in), _ptr(self.dx), _ptr(self.dw_router),
-            _ptr(self.ws) if self.ws.numel() else None, self.ws.numel(), _stream(stream)))
+            self._p, _ptr(dlogits), _ptr(x), _ptr(w_router), _ptr(dx_in), _own(self.dx), _own(self.dw_router),
+            _own(self.ws) if self.ws.numel() else None, self.ws.numel(), _stream(stream)))
         return dict(dx=self.dx, dw_router=self.dw_router)
 
 
@@ -629,8 +634,8 @@ class Decode:
             logits = self.logits
         _on_current(x)
         _check("moe_decode", lib().moe_decode(
-            self._p, _ptr(x), _ptr(w_router), _ptr(logits), _ptr(packed), _ptr(self.y), _ptr(self.idx),
-            _ptr(self.gate), _ptr(self.ws), self.ws.numel(), _stream(stream)))
+            self._p, _ptr(x), _ptr(w_router), _ptr(logits), _ptr(packed), _own(self.y), _own(self.idx),
+            _own(self.gate), _own(self.ws), self.ws.numel(), _stream(stream)))
         return self.y
 
     def experts(self, x, idx, gate, packed, stream=None):
@@ -641,7 +646,7 @@ class Decode:
         _expect(packed, (self.weight_bytes,), torch.uint8, "packed")
         _on_current(x)
         _check("moe_decode_experts", lib().moe_decode_experts(
-            self._p, _ptr(x), _ptr(idx), _ptr(gate), _ptr(packed), _ptr(self.y), _ptr(self.ws),
+            self._p, _ptr(x), _ptr(idx), _ptr(gate), _ptr(packed), _own(self.y), _own(self.ws),
             self.ws.numel(), _stream(stream)))
         return self.y
 

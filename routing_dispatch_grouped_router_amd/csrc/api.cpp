@@ -210,10 +210,8 @@ size_t bwd_aux_bytes(const moe_problem& p) {
     return bwd_layout(p).total + (learned ? align256(router_dw_part_bytes(p.act_dtype, p.T, p.d_model, p.n_experts)) : 0);
 }
 
-// Balance loss: float sums [blocks][E] and [blocks], then int counts likewise.
-size_t balance_part_bytes(const moe_problem& p) {
-    return align256((size_t)balance_blocks(p.T, p.n_experts) * (p.n_experts + 1) * 4);
-}
+// Balance loss: the partial sums (float), then the partial counts (int32).
+size_t balance_part_bytes(const moe_problem& p) { return align256(balance_part_floats(p.T, p.n_experts) * 4); }
 
 // Problems of the 4-bit decode form.
 int32_t check_decode(const moe_problem* p) {
@@ -992,6 +990,7 @@ int32_t moe_balance_loss(const moe_problem* p, const float* logits, const int32_
     int32_t st = check_problem(p);
     if (st) return st;
     if (!logits || !topk_idx || !counts || !loss || !ws) return MOE_ERR_NULL;
+    if (off_by(logits, 16) || off_by(ws, 16)) return MOE_ERR_ARG;
     const size_t part = balance_part_bytes(*p);
     if (ws_bytes < 2 * part) return MOE_ERR_WORKSPACE;
     return launched(launch_balance(logits, topk_idx, mask, p->T, p->n_experts, p->top_k, counts, loss,
@@ -1004,6 +1003,7 @@ int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, con
     int32_t st = check_problem(p);
     if (st) return st;
     if (!logits || !counts || !dloss || !dlogits) return MOE_ERR_NULL;
+    if (off_by(logits, 16) || off_by(dlogits, 16)) return MOE_ERR_ARG;
     return launched(launch_balance_bwd(logits, mask, counts, dloss, p->T, p->n_experts, p->top_k, dlogits,
                                        static_cast<hipStream_t>(stream)));
 }

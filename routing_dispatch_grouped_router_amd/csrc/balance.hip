@@ -13,7 +13,9 @@
 // (softmax statistics by cross-lane reductions in registers).  The forward
 // sums probabilities per workgroup, the second launch adds the workgroups'
 // partial sums; every sum runs in a fixed order and the counts are integers,
-// so the results are reproducible bit for bit.
+// so the results are reproducible bit for bit.  Up to a few MB of logits each
+// launch is a handful of memory latencies, not bandwidth, so the loads of
+// kTok tokens a group, and of all a thread's partial sums, are issued together.
 #include <algorithm>
 
 #include "moe_device.h"
@@ -23,22 +25,22 @@ namespace moe {
 
 namespace {
 
-constexpr int kBalBlocks = 512;   // partial rows: two workgroups per compute unit
+// The forward takes at most a workgroup of 16 waves per compute unit (few
+// partial rows for the second launch), the backward as many as it has tokens.
+constexpr int kBalBlocks = 256;
+constexpr int kBalThreads = 1024;
+constexpr int kTok = 2;           // tokens of a group in flight
 
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int m = G / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+    return __uint_as_float(group_reduce<G>(__float_as_uint(v), AddF32{}));
 }
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int m = G / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-    return v;
+    return __uint_as_float(group_reduce<G>(__float_as_uint(v), MaxF32{}));
 }
 
-// The V logits of this lane (experts r + G v, -inf past E), then their
+// The V logits of this lane (experts V r .. V r + V, -inf past E), then their
 // softmax and log-sum-exp over the group.  A row without a finite logit has
 // no distribution: p = 0, lse = 0.
 template <int G, int V>
@@ -61,97 +63,156 @@ __device__ __forceinline__ void row_softmax(const float (&l)[V], float (&p)[V], 
     lse = none ? 0.f : mx + logf(z);
 }
 
-template <int G, int V>
-__device__ __forceinline__ void load_logits(const float* logits, size_t t, int E, int r, float (&l)[V]) {
+template <int V>
+__device__ __forceinline__ void load_logits(const float* logits, size_t t, int E, int e0, float (&l)[V]) {
+    const float* row = logits + t * E;
+    if ((E & 3) == 0) {   // whole runs of four, 16 bytes aligned
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = r + G * v;
-        l[v] = logits[t * E + min(e, E - 1)];
+        for (int v = 0; v < V; v += 4) {
+            const f32x4 q = *reinterpret_cast<const f32x4*>(row + min(e0 + v, E - 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[v + i] = q[i];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = row[min(e0 + v, E - 1)];
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (r + G * v >= E) l[v] = -INFINITY;
+        if (e0 + v >= E) l[v] = -INFINITY;
 }
 
 }  // namespace
 
-// Workgroup b takes the tokens [b rows, (b + 1) rows), 256 / G at a time.
+// Workgroup b takes the tokens [b rows, (b + 1) rows), kBalThreads / G at a time.
 // part: psum [nblk][E], then z [nblk]; cnt: [nblk][E], then live [nblk].
 template <int G, int V>
-__global__ __launch_bounds__(256) void balance_partial_kernel(const float* __restrict__ logits,
-                                                              const int32_t* __restrict__ idx,
-                                                              const uint8_t* __restrict__ mask, int T, int E, int k,
-                                                              int rows, float* __restrict__ part,
-                                                              int32_t* __restrict__ cnt) {
-    constexpr int TA = 256 / G;
+__global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(const float* __restrict__ logits,
+                                                                      const int32_t* __restrict__ idx,
+                                                                      const uint8_t* __restrict__ mask, int T, int E,
+                                                                      int k, int rows, float* __restrict__ part,
+                                                                      int32_t* __restrict__ cnt) {
+    constexpr int TA = kBalThreads / G, NW = kBalThreads / 64;
     __shared__ int32_t s_cnt[kMaxExperts + 1];
-    __shared__ float s_p[256 * V];
-    __shared__ float s_z[TA];
-    const int tid = threadIdx.x, r = tid % G, grp = tid / G, nblk = gridDim.x;
-    for (int i = tid; i <= E; i += 256) s_cnt[i] = 0;
+    __shared__ float s_p[NW][G * V];
+    __shared__ float s_z[NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = tid % G, grp = tid / G, nblk = gridDim.x;
+    for (int i = tid; i <= E; i += kBalThreads) s_cnt[i] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * rows, t1 = min(T, t0 + rows);
     float ps[V], zs = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) ps[v] = 0.f;
     int live_n = 0;
-    for (int tb = t0; tb < t1; tb += TA) {
-        const int t = tb + grp;
-        const bool live = t < t1 && (mask == nullptr || mask[min(t, T - 1)] != 0);
-        float l[V], p[V], lse;
-        load_logits<G, V>(logits, (size_t)min(t, T - 1), E, r, l);
-        row_softmax<G, V>(l, p, lse);
-        if (live) {
+    for (int tb = t0; tb < t1; tb += TA * kTok) {
+        float l[kTok][V];
+        bool live[kTok];
 #pragma unroll
-            for (int v = 0; v < V; ++v) ps[v] += p[v];
-            zs = fmaf(lse, lse, zs);
-            ++live_n;
+        for (int u = 0; u < kTok; ++u) {
+            const int t = tb + TA * u + grp, tc = min(t, T - 1);
+            live[u] = t < t1 && (mask == nullptr || mask[tc] != 0);
+            load_logits<V>(logits, (size_t)tc, E, V * r, l[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+            float p[V], lse;
+            row_softmax<G, V>(l[u], p, lse);
+            if (live[u]) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) ps[v] += p[v];
+                zs = fmaf(lse, lse, zs);
+                ++live_n;
+            }
         }
     }
     // the tokens' choices: an index outside [0, E) is no choice
     const size_t i1 = (size_t)t1 * k;
-    for (size_t i = (size_t)t0 * k + tid; i < i1; i += 256) {
+    for (size_t i = (size_t)t0 * k + tid; i < i1; i += kBalThreads) {
         const int e = idx[i];
         if (e >= 0 && e < E && (mask == nullptr || mask[i / k] != 0)) atomicAdd(&s_cnt[e], 1);
     }
-    if (r == 0) {
-        s_z[grp] = zs;
+    // the wave's groups, then the waves in order
+    if (r != 0) {
+        zs = 0.f;
+        live_n = 0;
+    }
+#pragma unroll
+    for (int i = 32; i >= G; i >>= 1) {
+        zs += __shfl_xor(zs, i);
+        live_n += __shfl_xor(live_n, i);
+#pragma unroll
+        for (int v = 0; v < V; ++v) ps[v] += __shfl_xor(ps[v], i);
+    }
+    if (lane < G) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_p[wave][V * r + v] = ps[v];
+    }
+    if (lane == 0) {
+        s_z[wave] = zs;
         atomicAdd(&s_cnt[E], live_n);
     }
-    // s_p[grp][v][r]: this group's probabilities of expert r + G v
-#pragma unroll
-    for (int v = 0; v < V; ++v) s_p[(grp * V + v) * G + r] = ps[v];
     __syncthreads();
-    for (int e = tid; e < E; e += 256) {
+    for (int e = tid; e < E; e += kBalThreads) {
         float s = 0.f;
-        for (int g = 0; g < TA; ++g) s += s_p[g * V * G + e];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += s_p[w][e];
         part[(size_t)blockIdx.x * E + e] = s;
         cnt[(size_t)blockIdx.x * E + e] = s_cnt[e];
     }
     if (tid == 0) {
         float z = 0.f;
-        for (int g = 0; g < TA; ++g) z += s_z[g];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) z += s_z[w];
         part[(size_t)nblk * E + blockIdx.x] = z;
         cnt[(size_t)nblk * E + blockIdx.x] = s_cnt[E];
     }
 }
 
 // counts[E + 1] (the last one the live tokens) and loss[2] from the partial
-// sums: thread (e, c) adds expert e's over a chunk c of workgroups.
+// sums.  Workgroup b takes the experts [b EW, b EW + EW): thread (e, c) adds
+// expert e's over a chunk c of the partial rows.  One compute unit reads the
+// rows of 128 experts in a latency or two, those of 1024 in 25 us, so more
+// experts go to more workgroups and their shares of the balance loss (fpart)
+// to balance_sum_kernel.
+constexpr int kFinishExperts = 128;
+
 __global__ __launch_bounds__(1024) void balance_finish_kernel(const float* __restrict__ part,
                                                               const int32_t* __restrict__ cnt, int nblk, int E, int k,
-                                                              int32_t* __restrict__ counts, float* __restrict__ loss) {
+                                                              int32_t* __restrict__ counts, float* __restrict__ loss,
+                                                              float* __restrict__ fpart) {
     __shared__ float s_p[1024];
     __shared__ int32_t s_c[1024];
     __shared__ float s_z[16];
     __shared__ int32_t s_n[16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    // z and the live tokens: one wave each takes its share of the workgroups
     float z = 0.f;
     int n = 0;
     for (int b = tid; b < nblk; b += 1024) {
         z += part[(size_t)nblk * E + b];
         n += cnt[(size_t)nblk * E + b];
+    }
+    const int e0 = blockIdx.x * kFinishExperts, EW = min(kFinishExperts, E - e0);
+    const int NC = max(1, min(1024 / EW, nblk)), CS = (nblk + NC - 1) / NC;
+    const int e = tid % EW, c = tid / EW;
+    float p = 0.f;
+    int q = 0;
+    if (c < NC) {
+        constexpr int kB = 16;
+        const int b0 = c * CS, b1 = min(nblk, b0 + CS);
+        for (int b = b0; b < b1; b += kB) {
+            float pv[kB];
+            int qv[kB];
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                pv[u] = b + u < b1 ? part[(size_t)(b + u) * E + e0 + e] : 0.f;
+                qv[u] = b + u < b1 ? cnt[(size_t)(b + u) * E + e0 + e] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                p += pv[u];
+                q += qv[u];
+            }
+        }
     }
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) {
@@ -161,28 +222,6 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(const float* __res
     if (lane == 0) {
         s_z[wave] = z;
         s_n[wave] = n;
-    }
-    const int NC = max(1, min(1024 / E, nblk)), CS = (nblk + NC - 1) / NC;
-    const int e = tid % E, c = tid / E;
-    float p = 0.f;
-    int q = 0;
-    if (c < NC) {
-        constexpr int kB = 8;
-        const int b0 = c * CS, b1 = min(nblk, b0 + CS);
-        for (int b = b0; b < b1; b += kB) {
-            float pv[kB];
-            int qv[kB];
-#pragma unroll
-            for (int u = 0; u < kB; ++u) {
-                pv[u] = b + u < b1 ? part[(size_t)(b + u) * E + e] : 0.f;
-                qv[u] = b + u < b1 ? cnt[(size_t)(b + u) * E + e] : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < kB; ++u) {
-                p += pv[u];
-                q += qv[u];
-            }
-        }
     }
     s_p[tid] = p;
     s_c[tid] = q;
@@ -196,12 +235,12 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(const float* __res
     }
     const float inv = n > 0 ? 1.0f / (float)n : 0.f;
     float fp = 0.f;
-    if (tid < E) {
+    if (tid < EW) {
         for (int cc = 1; cc < NC; ++cc) {
-            p += s_p[cc * E + tid];
-            q += s_c[cc * E + tid];
+            p += s_p[cc * EW + tid];
+            q += s_c[cc * EW + tid];
         }
-        counts[tid] = q;
+        counts[e0 + tid] = q;
         fp = ((float)q * inv / (float)k) * (p * inv);
     }
 #pragma unroll
@@ -212,10 +251,21 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(const float* __res
     if (tid == 0) {
         fp = 0.f;
         for (int w = 0; w < 16; ++w) fp += s_z[w];
-        counts[E] = n;
-        loss[0] = (float)E * fp;
-        loss[1] = z * inv;
+        if (gridDim.x == 1) loss[0] = (float)E * fp;
+        else fpart[blockIdx.x] = fp;
+        if (blockIdx.x == 0) {
+            counts[E] = n;
+            loss[1] = z * inv;
+        }
     }
+}
+
+__global__ __launch_bounds__(64) void balance_sum_kernel(const float* __restrict__ fpart, int n, int E,
+                                                         float* __restrict__ loss) {
+    float v = threadIdx.x < (unsigned)n ? fpart[threadIdx.x] : 0.f;
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+    if (threadIdx.x == 0) loss[0] = (float)E * v;
 }
 
 template <int G, int V>
@@ -223,7 +273,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restric
                                                           const uint8_t* __restrict__ mask,
                                                           const int32_t* __restrict__ counts,
                                                           const float* __restrict__ dloss, int T, int E, int k,
-                                                          int rows, float* __restrict__ dlogits) {
+                                                          float* __restrict__ dlogits) {
     constexpr int TA = 256 / G;
     const int r = threadIdx.x % G, grp = threadIdx.x / G;
     const int n = counts[E];
@@ -232,23 +282,38 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restric
     float f[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        f[v] = r + G * v < E ? (float)counts[min(r + G * v, E - 1)] * inv / (float)k : 0.f;
-    const int t0 = blockIdx.x * rows, t1 = min(T, t0 + rows);
-    for (int tb = t0; tb < t1; tb += TA) {
-        const int t = tb + grp, tc = min(t, T - 1);
-        const bool live = mask == nullptr || mask[tc] != 0;
-        float l[V], p[V], lse;
-        load_logits<G, V>(logits, (size_t)tc, E, r, l);
-        row_softmax<G, V>(l, p, lse);
-        float fp = 0.f;
+        f[v] = V * r + v < E ? (float)counts[min(V * r + v, E - 1)] * inv / (float)k : 0.f;
+    const int tb = blockIdx.x * TA * kTok;
+    float l[kTok][V];
+    bool live[kTok];
+#pragma unroll
+    for (int u = 0; u < kTok; ++u) {
+        const int tc = min(tb + TA * u + grp, T - 1);
+        live[u] = mask == nullptr || mask[tc] != 0;
+        load_logits<V>(logits, (size_t)tc, E, V * r, l[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kTok; ++u) {
+        const int t = tb + TA * u + grp;
+        float p[V], lse, fp = 0.f;
+        row_softmax<G, V>(l[u], p, lse);
 #pragma unroll
         for (int v = 0; v < V; ++v) fp = fmaf(f[v], p[v], fp);
         fp = group_sum<G>(fp);
-        if (t >= t1) continue;   // whole groups
+        if (t >= T) continue;   // whole groups
+        float* row = dlogits + (size_t)t * E;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (r + G * v < E)
-                dlogits[(size_t)t * E + r + G * v] = live ? p[v] * fmaf(gb, f[v] - fp, gz * lse) : 0.f;
+        for (int v = 0; v < V; ++v) p[v] = live[u] ? p[v] * fmaf(gb, f[v] - fp, gz * lse) : 0.f;
+        if ((E & 3) == 0) {
+#pragma unroll
+            for (int v = 0; v < V; v += 4)
+                if (V * r + v < E)
+                    *reinterpret_cast<f32x4*>(row + V * r + v) = (f32x4){p[v], p[v + 1], p[v + 2], p[v + 3]};
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (V * r + v < E) row[V * r + v] = p[v];
+        }
     }
 }
 
@@ -262,9 +327,9 @@ int balance_lanes(int E) {
     return G;
 }
 
-// Tokens per workgroup: a multiple of those it takes at a time.
+// Tokens per workgroup of the forward: a multiple of those it takes at a time.
 int balance_rows(int T, int E) {
-    const int TA = 256 / balance_lanes(E);
+    const int TA = kBalThreads / balance_lanes(E);
     const int per = (T + kBalBlocks - 1) / kBalBlocks;
     return (per + TA - 1) / TA * TA;
 }
@@ -273,23 +338,27 @@ template <int G, int V>
 void partial_t(const float* logits, const int32_t* idx, const uint8_t* mask, int T, int E, int k, float* part,
                int32_t* cnt, hipStream_t s) {
     const int rows = balance_rows(T, E);
-    hipLaunchKernelGGL((balance_partial_kernel<G, V>), dim3((T + rows - 1) / rows), dim3(256), 0, s, logits, idx,
-                       mask, T, E, k, rows, part, cnt);
+    hipLaunchKernelGGL((balance_partial_kernel<G, V>), dim3((T + rows - 1) / rows), dim3(kBalThreads), 0, s, logits,
+                       idx, mask, T, E, k, rows, part, cnt);
 }
 
 template <int G, int V>
 void bwd_t(const float* logits, const uint8_t* mask, const int32_t* counts, const float* dloss, int T, int E, int k,
            float* dlogits, hipStream_t s) {
-    const int rows = balance_rows(T, E);
-    hipLaunchKernelGGL((balance_bwd_kernel<G, V>), dim3((T + rows - 1) / rows), dim3(256), 0, s, logits, mask, counts,
-                       dloss, T, E, k, rows, dlogits);
+    constexpr int per = 256 / G * kTok;
+    hipLaunchKernelGGL((balance_bwd_kernel<G, V>), dim3((T + per - 1) / per), dim3(256), 0, s, logits, mask, counts,
+                       dloss, T, E, k, dlogits);
 }
 
 }  // namespace
 
-int balance_blocks(int T, int E) {
+static int balance_blocks(int T, int E) {
     const int rows = balance_rows(T, E);
     return (T + rows - 1) / rows;
+}
+
+size_t balance_part_floats(int T, int E) {
+    return (size_t)balance_blocks(T, E) * (E + 1) + kMaxExperts / kFinishExperts;
 }
 
 hipError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t* mask, int T, int E, int k,
@@ -305,8 +374,10 @@ hipError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t
             if (E <= 256) partial_t<64, 4>(logits, idx, mask, T, E, k, part, cnt, s);
             else partial_t<64, 16>(logits, idx, mask, T, E, k, part, cnt, s);
     }
-    hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(1024), 0, s, part, cnt, balance_blocks(T, E), E, k, counts,
-                       loss);
+    const int nblk = balance_blocks(T, E), nf = (E + kFinishExperts - 1) / kFinishExperts;
+    float* fpart = part + (size_t)nblk * (E + 1);
+    hipLaunchKernelGGL(balance_finish_kernel, dim3(nf), dim3(1024), 0, s, part, cnt, nblk, E, k, counts, loss, fpart);
+    if (nf > 1) hipLaunchKernelGGL(balance_sum_kernel, dim3(1), dim3(64), 0, s, fpart, nf, E, loss);
     return hipGetLastError();
 }
 

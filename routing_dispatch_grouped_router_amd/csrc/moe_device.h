@@ -37,6 +37,41 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// Cross-lane steps inside aligned groups of G lanes (G a power of two <= 64):
+// quad permutations and the row mirrors are DPP operand modifiers (no LDS
+// round trip); only groups wider than a 16-lane row use ds_bpermute.  Every
+// lane of a group ends with the same value.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int G, typename Op>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, Op op) {
+    if constexpr (G >= 2) v = op(v, dpp_u32<0xB1>(v));     // quad_perm [1,0,3,2]: lane ^ 1
+    if constexpr (G >= 4) v = op(v, dpp_u32<0x4E>(v));     // quad_perm [2,3,0,1]: lane ^ 2
+    if constexpr (G >= 8) v = op(v, dpp_u32<0x141>(v));    // row_half_mirror: the other quad of 8
+    if constexpr (G >= 16) v = op(v, dpp_u32<0x140>(v));   // row_mirror: the other half of 16
+    if constexpr (G >= 32) v = op(v, (uint32_t)__shfl_xor((int)v, 16));
+    if constexpr (G >= 64) v = op(v, (uint32_t)__shfl_xor((int)v, 32));
+    return v;
+}
+struct MaxU32 {
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+};
+struct MinU32 {
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; }
+};
+struct AddF32 {   // a + b == b + a bitwise, so both lanes of a pair agree
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }
+};
+struct MaxF32 {
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+};
+
 // ---------------------------------------------------------------- MXFP8 (OCP MX v1.0)
 
 // Shared block exponent floor(log2(amax)) - 8 clamped to [-127, 127], from the

@@ -243,8 +243,8 @@ hipError_t launch_norm_bwd(int act, const void* dy, const void* dsum, const void
 
 // ---------------------------------------------------------------- balance loss (balance.hip)
 
-// Partial rows of the forward: part holds balance_blocks (E + 1) float, cnt as many int32.
-int balance_blocks(int T, int E);
+// Scratch of the forward: part holds this many float, cnt as many int32.
+size_t balance_part_floats(int T, int E);
 hipError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t* mask, int T, int E, int k,
                           int32_t* counts, float* loss, float* part, int32_t* cnt, hipStream_t s);
 hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t* counts, const float* dloss,

@@ -16,7 +16,10 @@
 //   ds = rstd (u - n mean(u n)) + dsum,   dw = sum over tokens of dy n.
 //
 // All of it is bound by HBM: every tensor is read or written once.  A row
-// stays in registers between its reduction and its output.
+// stays in registers between its reduction and its output.  Forward, T = 32768,
+// d = 2048, MXFP8 rows with residual and codes: 94 us, 6.4 TB/s; backward,
+// T = 16384, d = 4096, bf16 with dsum: 101 us, 5.3 TB/s (a 2 GiB copy runs at
+// 4.9 TB/s on the same card).
 #include <algorithm>
 
 #include "moe_device.h"
@@ -63,6 +66,23 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     return v;
 }
 
+// 16 bytes of a stream; NT: past the caches, for tensors that they cannot hold
+// for whoever reads them next.
+template <bool NT>
+__device__ __forceinline__ u32x4 stream_load(const u32x4* p) {
+    return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT>
+__device__ __forceinline__ void stream_store(u32x4* p, const u32x4& v) {
+    if (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
+// A tensor as large as the eight 4 MB L2s together.  Forward, T = 16384,
+// d = 4096, bf16: 94 us through the caches, 89 past them; T = 32768, d = 2048,
+// MXFP8 with codes: 105 and 94; T = 2048, d = 4096 (17 MB): 11.0 and 13.3.
+bool past_caches(int T, int chunks) { return (size_t)T * chunks * 16 >= (size_t)32 << 20; }
+
 struct NormArgs {
     const u32x4* x;
     const u32x4* r;      // NULL: no residual
@@ -77,8 +97,10 @@ struct NormArgs {
 };
 
 // TPR threads per row (a wave, or a workgroup of 256); CH chunks per thread
-// stay in registers, chunks past TPR CH of a longer row are read again.
-template <bool BF, int TPR, int CH>
+// stay in registers, chunks past TPR CH of a longer row are read again.  A wave
+// takes rows of up to two chunks a lane: with eight (4096 bf16 values) the
+// registers leave too few waves to cover the loads (103 us against 94).
+template <bool BF, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     constexpr int NV = BF ? 8 : 4;
     __shared__ float red[4];
@@ -91,8 +113,8 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int g = 0; g < CH; ++g) {
         const int c = min(lt + TPR * g, a.chunks - 1);   // clamped chunks are loaded, not used
-        xr[g] = a.x[row + c];
-        if (a.r) rr[g] = a.r[row + c];
+        xr[g] = stream_load<NT>(a.x + row + c);
+        if (a.r) rr[g] = stream_load<NT>(a.r + row + c);
     }
     float ss = 0.f;
 #pragma unroll
@@ -127,13 +149,13 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     const float rstd = 1.0f / sqrtf(row_sum<TPR>(ss, red) * a.inv_d + a.eps);
     if (a.rstd && lt == 0) a.rstd[t] = rstd;
     auto emit = [&](int c, const float (&s)[8]) {
-        if (a.sum) a.sum[row + c] = pack16<BF>(s);
+        if (a.sum) stream_store<NT>(a.sum + row + c, pack16<BF>(s));
         float wv[8], o[8];
         unpack16<BF>(a.w[c], wv);
 #pragma unroll
         for (int i = 0; i < NV; ++i) o[i] = s[i] * rstd * wv[i];
         const u32x4 yp = pack16<BF>(o);
-        if (a.y) a.y[row + c] = yp;
+        if (a.y) stream_store<NT>(a.y + row + c, yp);
         if constexpr (BF) {
             if (a.q) {   // d % 128 == 0: 16 lanes hold one 128-wide slice, 4 lanes one block of 32
                 float f[8];
@@ -181,7 +203,10 @@ struct NormBwdArgs {
 // Rows of at most TPR CH chunks: a group of TPR threads walks `rows`
 // consecutive rows, keeping its columns' weights and weight-gradient sums in
 // registers; the workgroup's groups are added in order into one partial row.
-template <bool BF, int TPR, int CH>
+// A workgroup per row once a row has more than two chunks a lane (a wave per
+// row of 4096 bf16 values needs 370 registers: one wave a SIMD, 120 us against
+// 111 at T = 16384); streams that exceed the caches non-temporal (111 -> 101).
+template <bool BF, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int NV = BF ? 8 : 4;
     constexpr int NG = 256 / TPR;
@@ -202,9 +227,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
         for (int g = 0; g < CH; ++g) {
             const int c = min(lt + TPR * g, a.chunks - 1);
-            sr[g] = a.s[row + c];
-            yr[g] = a.dy[row + c];
-            if (a.dsum) er[g] = a.dsum[row + c];
+            sr[g] = stream_load<NT>(a.s + row + c);
+            yr[g] = stream_load<NT>(a.dy + row + c);
+            if (a.dsum) er[g] = stream_load<NT>(a.dsum + row + c);
         }
         const float rstd = a.rstd[t];
         float dot = 0.f;
@@ -238,7 +263,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 o[i] = rstd * (yv[i] * wv[g][i] - sv[i] * rstd * m);
                 if (a.dsum) o[i] += ev[i];
             }
-            a.ds[row + c] = pack16<BF>(o);
+            stream_store<NT>(a.ds + row + c, pack16<BF>(o));
         }
     }
     if constexpr (NG > 1) {
@@ -332,7 +357,7 @@ __global__ __launch_bounds__(1024) void norm_dweight_reduce_kernel(const float* 
                                                                    float* __restrict__ dw) {
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
-    constexpr int kB = 8;
+    constexpr int kB = 32;   // all of a wave's rows at once (n <= 512)
     float s = 0.f;
     for (int b = wave; b < n; b += 16 * kB) {
         float v[kB];
@@ -362,12 +387,12 @@ constexpr int kNormPartials = 512;   // two workgroups per compute unit
 
 NormBwdPlan norm_bwd_plan(int T, int chunks) {
     NormBwdPlan p{};
-    if (chunks <= 64 * 8) {
+    if (chunks <= 64 * 2) {
         p.tpr = 64;
-        p.ch = chunks <= 64 ? 1 : (chunks <= 128 ? 2 : (chunks <= 256 ? 4 : 8));
+        p.ch = chunks <= 64 ? 1 : 2;
     } else if (chunks <= 256 * 4) {
         p.tpr = 256;
-        p.ch = 4;
+        p.ch = chunks <= 256 ? 1 : (chunks <= 512 ? 2 : 4);
     }
     const int groups = kNormPartials * (p.tpr == 64 ? 4 : 1);
     p.rows = (T + groups - 1) / groups;
@@ -376,36 +401,39 @@ NormBwdPlan norm_bwd_plan(int T, int chunks) {
     return p;
 }
 
-template <bool BF>
+template <bool BF, bool NT>
 void launch_norm_t(const NormArgs& a, hipStream_t s) {
-    const dim3 b(256);
-    if (a.chunks <= 64 * 8 && (a.T >= 1024 || a.chunks <= 64)) {
-        const dim3 g((a.T + 3) / 4);
-        if (a.chunks <= 64) hipLaunchKernelGGL((norm_kernel<BF, 64, 1>), g, b, 0, s, a);
-        else if (a.chunks <= 128) hipLaunchKernelGGL((norm_kernel<BF, 64, 2>), g, b, 0, s, a);
-        else if (a.chunks <= 256) hipLaunchKernelGGL((norm_kernel<BF, 64, 4>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((norm_kernel<BF, 64, 8>), g, b, 0, s, a);
-    } else if (a.chunks <= 512) {
-        hipLaunchKernelGGL((norm_kernel<BF, 256, 2>), dim3(a.T), b, 0, s, a);
+    const dim3 b(256), rows(a.T), waves((a.T + 3) / 4);
+    if (a.chunks <= 64) hipLaunchKernelGGL((norm_kernel<BF, 64, 1, NT>), waves, b, 0, s, a);
+    else if (a.chunks <= 128 && a.T >= 1024) hipLaunchKernelGGL((norm_kernel<BF, 64, 2, NT>), waves, b, 0, s, a);
+    else if (a.chunks <= 256) hipLaunchKernelGGL((norm_kernel<BF, 256, 1, NT>), rows, b, 0, s, a);
+    else if (a.chunks <= 512) hipLaunchKernelGGL((norm_kernel<BF, 256, 2, NT>), rows, b, 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<BF, 256, 4, NT>), rows, b, 0, s, a);
+}
+
+template <bool BF, bool NT>
+void launch_norm_bwd_rows(const NormBwdArgs& a, const NormBwdPlan& p, hipStream_t s) {
+    const dim3 b(256), g(p.blocks);
+    const size_t lds = p.tpr == 64 ? (size_t)3 * a.chunks * 16 * (BF ? 2 : 1) : 0;
+    if (p.tpr == 64) {
+        if (p.ch == 1) hipLaunchKernelGGL((norm_bwd_kernel<BF, 64, 1, NT>), g, b, lds, s, a);
+        else hipLaunchKernelGGL((norm_bwd_kernel<BF, 64, 2, NT>), g, b, lds, s, a);
     } else {
-        hipLaunchKernelGGL((norm_kernel<BF, 256, 4>), dim3(a.T), b, 0, s, a);
+        if (p.ch == 1) hipLaunchKernelGGL((norm_bwd_kernel<BF, 256, 1, NT>), g, b, 0, s, a);
+        else if (p.ch == 2) hipLaunchKernelGGL((norm_bwd_kernel<BF, 256, 2, NT>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((norm_bwd_kernel<BF, 256, 4, NT>), g, b, 0, s, a);
     }
 }
 
 template <bool BF>
 void launch_norm_bwd_t(const NormBwdArgs& a, const NormBwdPlan& p, hipStream_t s) {
-    const dim3 b(256), g(p.blocks);
-    const size_t lds = p.tpr == 64 ? (size_t)3 * a.chunks * 16 * (BF ? 2 : 1) : 0;
-    if (p.tpr == 64) {
-        if (p.ch == 1) hipLaunchKernelGGL((norm_bwd_kernel<BF, 64, 1>), g, b, lds, s, a);
-        else if (p.ch == 2) hipLaunchKernelGGL((norm_bwd_kernel<BF, 64, 2>), g, b, lds, s, a);
-        else if (p.ch == 4) hipLaunchKernelGGL((norm_bwd_kernel<BF, 64, 4>), g, b, lds, s, a);
-        else hipLaunchKernelGGL((norm_bwd_kernel<BF, 64, 8>), g, b, lds, s, a);
-    } else if (p.tpr == 256) {
-        hipLaunchKernelGGL((norm_bwd_kernel<BF, 256, 4>), g, b, 0, s, a);
+    if (p.tpr == 0) {
+        hipLaunchKernelGGL((norm_bwd_long_kernel<BF>), dim3(a.T), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((norm_dweight_long_kernel<BF>), dim3((a.chunks + 255) / 256, p.blocks), dim3(256), 0, s, a);
+    } else if (past_caches(a.T, a.chunks)) {   // (T = 8000, d = 512, 8 MB: 11.3 us through them, 12.4 past them)
+        launch_norm_bwd_rows<BF, true>(a, p, s);
     } else {
-        hipLaunchKernelGGL((norm_bwd_long_kernel<BF>), dim3(a.T), b, 0, s, a);
-        hipLaunchKernelGGL((norm_dweight_long_kernel<BF>), dim3((a.chunks + 255) / 256, p.blocks), b, 0, s, a);
+        launch_norm_bwd_rows<BF, false>(a, p, s);
     }
 }
 
@@ -418,8 +446,11 @@ hipError_t launch_norm(int act, const void* x, const void* residual, const void*
                      static_cast<const u32x4*>(weight), static_cast<u32x4*>(sum), static_cast<u32x4*>(y),
                      static_cast<uint2*>(q), reinterpret_cast<uint32_t*>(q_scale), rstd, T, d / (bf ? 8 : 4),
                      1.0f / (float)d, eps};
-    if (bf) launch_norm_t<true>(a, s);
-    else launch_norm_t<false>(a, s);
+    const bool nt = past_caches(T, a.chunks);
+    if (bf && nt) launch_norm_t<true, true>(a, s);
+    else if (bf) launch_norm_t<true, false>(a, s);
+    else if (nt) launch_norm_t<false, true>(a, s);
+    else launch_norm_t<false, false>(a, s);
     return hipGetLastError();
 }
 

@@ -77,11 +77,15 @@ def test_balance():
     for i in (0, 1, 3, 4, 5):
         assert _call("moe_balance_loss", _p(), *_swap(ok, i, None)) == -1
     assert _call("moe_balance_loss", _p(), *_swap(ok, 6, 8)) == -4
+    for i in (0, 5):
+        assert _call("moe_balance_loss", _p(), *_swap(ok, i, ODD)) == -7
     assert _call("moe_balance_loss", _p(E=1025), *ok) == -2
     # logits, mask, counts, dloss, dlogits, stream
     ok = [F, None, F, F, F, None]
     for i in (0, 2, 3, 4):
         assert _call("moe_balance_loss_backward", _p(), *_swap(ok, i, None)) == -1
+    for i in (0, 4):
+        assert _call("moe_balance_loss_backward", _p(), *_swap(ok, i, ODD)) == -7
 
 
 def test_router_backward():

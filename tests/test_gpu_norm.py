@@ -37,7 +37,7 @@ def _problem(T, d, act):
 
 # one token, a few, counts around the tile sizes, widths of every register variant and beyond them
 SHAPES = [(1, 64), (1, 4096), (3, 192), (5, 512), (130, 576), (1023, 1024), (1025, 2048), (2100, 4096), (70, 8192),
-          (9, 16448), (2, 32768)]
+          (9, 16448), (2, 32768), (4200, 4096)]
 
 
 @pytest.mark.parametrize("residual", [False, True])
@@ -106,7 +106,7 @@ def test_norm_of_rows_with_nonfinite_values_leaves_the_others():
 
 
 BWD_SHAPES = [(1, 64), (1, 4096), (3, 192), (130, 576), (1000, 256), (2100, 1024), (5000, 128), (600, 4096), (70, 8192),
-              (9, 16448), (700, 9216)]
+              (9, 16448), (700, 9216), (4200, 4096)]
 
 
 @pytest.mark.parametrize("dsum", [False, True])
@@ -133,7 +133,7 @@ def test_norm_backward(T, d, act, dsum):
     u, n = np.abs(dy64 * w64), np.abs(s64 * r64[:, None])
     mag = r64[:, None] * (u + n * (u * n).mean(1, keepdims=True)) + (0 if ds_in is None else np.abs(as_f64(ds_in)))
     _close("ds", g["ds"], ds_ref, HALF[act] * np.abs(ds_ref) + 160 * U * mag)
-    # the weight gradient: T <= 5000 rows, at most 16 per thread, then 4 and 512 / 16 partial sums and 16 waves
+    # the weight gradient: T <= 5000 rows, at most 10 per thread, then 4 and 512 / 16 partial sums and 16 waves
     _close("dweight", g["dweight"], dw_ref, 80 * U * (np.abs(dy64) * n).sum(0))
 
 

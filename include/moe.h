@@ -474,7 +474,8 @@ int32_t moe_norm(const moe_problem* p, const void* x, const void* residual, cons
  *   rstd    : device float32 [T] of the forward
  *   ds      : device [T, d] out, may be dy or dsum (in place)
  *   dweight : device float32 [d] out
- *   ws      : device, moe_norm_backward_workspace_bytes (host-only query)
+ *   ws      : device, moe_norm_backward_workspace_bytes (host-only query);
+ *             calls sharing a workspace must not overlap, here and below
  * Sums run in a fixed order (bitwise reproducible).  Tensors 16-byte aligned
  * (rstd 4).  Errors: MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an
  * unaligned pointer or ds == s. */
@@ -552,7 +553,8 @@ int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const vo
  * arguments as moe_backward; ws_bytes >= moe_backward_aux_workspace_bytes.
  * With both NULL it is moe_backward.  Errors: as moe_backward; MOE_ERR_DTYPE /
  * MOE_ERR_SHAPE for xq on a problem moe_forward_quantized does not take;
- * MOE_ERR_ARG for an unaligned xq, or for dlogits_aux == dlogits. */
+ * MOE_ERR_ARG for an unaligned xq (16), for dlogits_aux == dlogits, and with
+ * dlogits_aux for dlogits, w_router, x, dx or ws not 16-byte aligned. */
 int32_t moe_backward_aux_workspace_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, const void* w_router,
                          const void* packed_w, const void* packed_bwd, const int32_t* topk_idx,
@@ -587,10 +589,11 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  *   x [T, d] bf16; w_router [d, E] bf16 (NULL with MOE_LOGITS_GIVEN);
  *   logits float32 [T, E]; topk_idx int32 [T, k]; topk_gate float32 [T, k];
  *   y [T, d] bf16 out (not x); ws: moe_decode_workspace_bytes (host-only query)
- * x, w_router, logits, packed, y and ws are 16-byte aligned.  Results do not depend on the other
- * tokens of the call.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T over the limit,
- * d or H not a multiple of 128), MOE_ERR_DTYPE, MOE_ERR_WORKSPACE,
- * MOE_ERR_ARG for an unaligned pointer or y == x. */
+ * x, w_router, logits, packed, y and ws are 16-byte aligned.  A token's result
+ * does not depend on the other tokens of the call.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_SHAPE (T over the limit, d or H not a multiple of 128, T k max(d, 2 H)
+ * bfloat16 not below 2^32 bytes), MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_ARG
+ * for an unaligned pointer or y == x. */
 #define MOE_DECODE_MAX_TOKENS 256
 int32_t moe_decode_weight_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_decode_workspace_bytes(const moe_problem* p, size_t* bytes);

@@ -933,6 +933,9 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
     int32_t st = MOE_OK;
     if (xq && (st = check_quantized(p))) return st;
     if (off_by(xq, 16) || (dlogits_aux && dlogits_aux == dlogits)) return MOE_ERR_ARG;
+    // the dense router gradients read and write these 16 bytes at a time
+    if (dlogits_aux && (off_by(dlogits, 16) || off_by(w_router, 16) || off_by(x, 16) || off_by(dx, 16) || off_by(ws, 16)))
+        return MOE_ERR_ARG;
     return backward_impl(p, dy, x, w_router, packed_w, packed_bwd, topk_idx, topk_gate, offsets, pos, fwd_ws,
                          fwd_ws_bytes, dx, dlogits, dw_gate, dw_up, dw_down, dw_router, ws, ws_bytes, stream,
                          dlogits_aux, xq);

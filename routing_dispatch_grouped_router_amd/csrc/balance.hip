@@ -268,12 +268,14 @@ __global__ __launch_bounds__(64) void balance_sum_kernel(const float* __restrict
     if (threadIdx.x == 0) loss[0] = (float)E * v;
 }
 
+// dlogits may be logits: a group reads its row before it writes it, and what the
+// groups past T read of row T - 1 is not used.
 template <int G, int V>
-__global__ __launch_bounds__(256) void balance_bwd_kernel(const float* __restrict__ logits,
+__global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
                                                           const uint8_t* __restrict__ mask,
                                                           const int32_t* __restrict__ counts,
                                                           const float* __restrict__ dloss, int T, int E, int k,
-                                                          float* __restrict__ dlogits) {
+                                                          float* dlogits) {
     constexpr int TA = 256 / G;
     const int r = threadIdx.x % G, grp = threadIdx.x / G;
     const int n = counts[E];

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
     constexpr int TA = BF ? 1 : 3;
     constexpr int kTile = 32 * 32 + 32;                 // bytes of a 16-column block, padded
     constexpr int NX = BF ? 1 : 2;                      // 16-byte loads of 8 columns
-    constexpr int PD = 2;
+    constexpr int PD = BF && NT < 4 ? 4 : 2;            // as many as the registers of two waves a SIMD hold
     constexpr int XI = CT / 64;                         // 8-column items of a thread: 32 tokens x CT / 8 chunks
     constexpr int WE = NT == 4 ? 2 : 1, WC = 4 / WE;    // waves over the experts, over the columns
     constexpr int MT = CT / WC / 16, NW = NT / WE;      // a wave's blocks
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
 // dw[i] = sum over the S token ranges of part[.][i], in order.
 __global__ __launch_bounds__(256) void router_dw_reduce_kernel(const float* __restrict__ part, int S, size_t n,
                                                                float* __restrict__ dw) {
-    constexpr int kB = 8;
+    constexpr int kB = 32;   // a latency or two for all ranges
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
         float s = 0.f;
         for (int b = 0; b < S; b += kB) {

@@ -135,7 +135,8 @@ def test_backward_aux():
     assert _call(name, p, *_swap(ok, 0, None)) == -1
     assert _call(name, p, *_swap(ok, 18, need - 1)) == -4
     assert _call(name, p, *_swap(ok, 20, F)) == -7                                     # aux is dlogits
-    assert _call(name, p, *_swap(ok, 21, ODD)) == -7
+    for i in (1, 2, 11, 12, 17, 21):                                                   # x, w_router, dx, dlogits, ws, xq
+        assert _call(name, p, *_swap(ok, i, ODD)) == -7
     assert _call(name, _p(), *ok) == -3                                                # codes of a bf16 block
     assert _call(name, _p(act="mxfp8", d=128), *ok) == -2
 
@@ -143,7 +144,10 @@ def test_backward_aux():
 def test_decode():
     n = ctypes.c_size_t()
     for kw, st in [(dict(T=257), -2), (dict(d=192), -2), (dict(H=192), -2), (dict(act="f32"), -3),
-                   (dict(identity=True), -3), (dict(T=256), 0), (dict(act="mxfp8"), 0)]:
+                   (dict(identity=True), -3), (dict(T=256), 0), (dict(act="mxfp8"), 0),
+                   # h [T k][2][H] bfloat16 reaches 2^32 bytes
+                   (dict(T=256, E=16, k=16, d=128, H=1 << 18, act="mxfp8"), -2),
+                   (dict(T=255, E=16, k=16, d=128, H=1 << 18, act="mxfp8"), 0)]:
         assert _call("moe_decode_workspace_bytes", _p(**kw), ctypes.byref(n)) == st
     p = _p(logits_given=True)
     assert B.decode_weight_bytes(p) == 8 * 3 * 256 * 256 * 17 // 32

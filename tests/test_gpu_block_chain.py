@@ -28,7 +28,7 @@ TOL = {"f32": 1e-5, "bf16": 2e-2, "mxfp8": 2e-2}
 class Step:
     """A training step of a pre-norm block: everything preallocated, run() enqueues it."""
 
-    def __init__(self, w: W.Workload, quantized: bool, padded: int = 0):
+    def __init__(self, w: W.Workload, quantized: bool, padded: int = 0, keep: bool = False):
         self.w = w
         host = W.make_inputs(w)
         rng = np.random.default_rng(w.seed + 99)
@@ -44,7 +44,8 @@ class Step:
             self.mask = torch.ones(w.T, dtype=torch.uint8, device=DEV)
             self.mask[-padded:] = 0
         self.dloss = torch.tensor(DLOSS, device=DEV)
-        p = self.p = B.problem(w.T, w.d, w.E, w.k, w.H, w.act, logits_given=w.router != "learned")
+        p = self.p = B.problem(w.T, w.d, w.E, w.k, w.H, w.act, logits_given=w.router != "learned",
+                                 keep_gate_up=keep)
         d = self.dev
         self.packed = B.pack_weights(p, d["w_gate"], d["w_up"], d["w_down"])
         self.packed_bwd = B.pack_weights_backward(p, d["w_gate"], d["w_up"], d["w_down"])
@@ -131,10 +132,11 @@ def test_training_step(w, quantized, padded):
     _close("dweight", out["dweight"], dweight, tol)
 
 
+@pytest.mark.parametrize("keep", [False, True], ids=["recompute", "keep_gate_up"])
 @pytest.mark.parametrize("w", [c[0] for c in CASES if c[1]], ids=[c[0].name for c in CASES if c[1]])
-def test_quantised_rows_give_the_same_block(w):
+def test_quantised_rows_give_the_same_block(w, keep):
     """moe_forward_quantized and its backward, bit for bit those of the bf16 rows."""
-    st = Step(w, True)
+    st = Step(w, True, keep=keep)
     out = {k: (None if v is None else v.clone()) for k, v in st.run().items()}
     idx, pos = st.fwd.idx.clone(), st.fwd.pos.clone()
     st.norm.q = st.norm.q_scale = None
@@ -162,6 +164,28 @@ def test_aux_of_zeros_is_the_sparse_backward():
         assert torch.equal(dense[k], sparse[k]), k
     for k, tol in (("dx", 2.0 ** -7), ("dw_router", 1e-5)):    # one bf16 step; float32 sums in another order
         _close(k, dense[k], as_f64(sparse[k]), tol)
+
+
+def test_two_steps_at_once():
+    """Two steps with buffers of their own on two streams, neither waiting for the other."""
+    steps = [Step(*CASES[4]), Step(*CASES[1])]
+    want = []
+    for st in steps:
+        st.run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in _outputs(st)])
+    for st in steps:
+        for t in _outputs(st):
+            t.fill_(3)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(3):
+        for st, s in zip(steps, streams):
+            with torch.cuda.stream(s):
+                st.run()
+    torch.cuda.synchronize()
+    for st, w in zip(steps, want):
+        assert all(torch.equal(a, b) for a, b in zip(_outputs(st), w))
 
 
 def _graph_replays(run, outputs, n=4):

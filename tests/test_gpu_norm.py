@@ -71,8 +71,9 @@ def test_norm(T, d, act, residual):
         assert op.q is None
 
 
-def test_norm_in_place_and_codes_only():
-    T, d = 300, 512
+# 512: a row in registers; 16512: rows read twice; (4200, 4096): streamed past the caches
+@pytest.mark.parametrize("T, d", [(300, 512), (5, 16512), (4200, 4096)])
+def test_norm_in_place_and_codes_only(T, d):
     rng = np.random.default_rng(1)
     x, r, w = (_rand(rng, s, "mxfp8").to(DEV) for s in ((T, d), (T, d), (d,)))
     op = B.Norm(_problem(T, d, "mxfp8"), DEV)

@@ -60,7 +60,9 @@ def _check_balance(logits, idx, mask, k, dloss=(0.3, 0.05)):
         tol[live] = (64 + 2 * np.minimum(span, 100)) * U * mag + 2.0 ** -126 / n * (E + 2 * np.abs(lse)[:, None])
     _close("dlogits", dl, ref, tol)
     assert not as_f64(dl)[~live].any()
-    return op
+    want = dl.clone()
+    op.dlogits = l                                           # in place
+    assert torch.equal(op.backward(l, g, mask=m), want)
 
 
 # the lanes-per-token variants (E 1 .. 1024), token counts of one workgroup and of many

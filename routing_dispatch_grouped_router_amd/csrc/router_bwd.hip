@@ -83,6 +83,19 @@ __device__ __forceinline__ void load_terms(const void* p, size_t i, int n, bool 
     }
 }
 
+// The same with all eight valid and 16 bytes aligned.
+template <bool BF>
+__device__ __forceinline__ void load_terms_full(const void* p, uint32_t i, bf16x8 (&o)[BF ? 1 : 3]) {
+    if constexpr (BF) {
+        o[0] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p) + i);
+    } else {
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i + 4);
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        split3(v, o);
+    }
+}
+
 }  // namespace
 
 // dx: a workgroup owns 64 tokens and 256 columns, a wave 32 by 128 of them, as
@@ -90,7 +103,7 @@ __device__ __forceinline__ void load_terms(const void* p, size_t i, int n, bool 
 // block j is column 8 n + j, so that a lane's eight blocks hold 8 consecutive
 // columns of a token and sixteen lanes 128: add is read and dx written in whole
 // lines (a lane layout with a row per lane cost the memory pipe an access per
-// lane, 126 us at T = 16384, d = 4096, E = 64).  Both operands pass through LDS
+// lane, 126 us at T = 16384, d = 4096, E = 64; 75 us so, 3.6 TB/s).  Both operands pass through LDS
 // in fragment order, 32 experts at a time, loaded in whole 64- and 128-byte
 // pieces and split once for the workgroup; two buffers, the next experts' loads
 // in flight during a step's products.  `add`: row t of add (pos NULL; requested
@@ -114,12 +127,28 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
 
     // thread: experts 8 (tid % 4) .. of token tid / 4 and of columns tid / 4 + 64 i
     const int lr = tid >> 2, lq = tid & 3;
+    // (uniform bases and 32-bit lane offsets, and a path without the test for the last expert: address and select
+    // instructions held this kernel up, 79 us with a 64-bit offset and a test a load at the size above, 75 us so)
+    const float* dl0 = dL + (size_t)t0 * E;
+    const char* w0 = static_cast<const char*>(w) + (size_t)c0 * E * (BF ? 2 : 4);
+    const uint32_t dlo = (uint32_t)min(lr, T - 1 - t0) * (uint32_t)E + 8 * lq;
+    uint32_t wo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wo[i] = (uint32_t)min(lr + 64 * i, d - 1 - c0) * (uint32_t)E + 8 * lq;
     bf16x8 ra[3], rw[4][TA];
     auto load = [&](int e0) {
-        const int e = e0 + 8 * lq, n = E - e;
-        load_terms<false>(dL, (size_t)min(t0 + lr, T - 1) * E + e, n, vec, ra);
+        const int n = E - e0 - 8 * lq;
+        const float* dle = dl0 + e0;
+        const char* we = w0 + (size_t)e0 * (BF ? 2 : 4);
+        if (vec && e0 + 32 <= E) {   // no expert is past the last
+            load_terms_full<false>(dle, dlo, ra);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_terms<BF>(w, (size_t)min(c0 + lr + 64 * i, d - 1) * E + e, n, vec, rw[i]);
+            for (int i = 0; i < 4; ++i) load_terms_full<BF>(we, wo[i], rw[i]);
+        } else {
+            load_terms<false>(dle, dlo, n, vec, ra);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_terms<BF>(we, wo[i], n, vec, rw[i]);
+        }
     };
     auto stage = [&](int buf) {
 #pragma unroll
@@ -173,6 +202,10 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
     }
     if (!in_cols) return;
     u32x4* dst = static_cast<u32x4*>(dx);
+    auto value = [](const u32x4 (&c)[NC], int j) {   // value j of 8 in memory order
+        return BF ? __uint_as_float((j & 1) ? (c[0][j / 2] & 0xFFFF0000u) : (c[0][j / 2] << 16))
+                  : __uint_as_float(c[NC == 1 ? 0 : j / 4][j % 4]);
+    };
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -180,28 +213,20 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
             const int t = wt + 16 * mt + 4 * q + i;
             if (t >= T) continue;
             float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.f;
-            auto plus = [&](const u32x4& c, int g) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (BF) {
-                        v[2 * h] += __uint_as_float(c[h] << 16);
-                        v[2 * h + 1] += __uint_as_float(c[h] & 0xFFFF0000u);
-                    } else {
-                        v[4 * g + h] += __uint_as_float(c[h]);
-                    }
-                }
-            };
             if (pos) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.f;
                 for (int s = 0; s < k; ++s) {
                     const size_t r = (size_t)pos[(size_t)t * k + s];
+                    u32x4 c[NC];
 #pragma unroll
-                    for (int g = 0; g < NC; ++g) plus(src[r * row_chunks + cb + g], g);
+                    for (int g = 0; g < NC; ++g) c[g] = src[r * row_chunks + cb + g];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += value(c, j);
                 }
-            } else if (src) {
+            } else {
 #pragma unroll
-                for (int g = 0; g < NC; ++g) plus(base[mt][i][g], g);
+                for (int j = 0; j < 8; ++j) v[j] = src ? value(base[mt][i], j) : 0.f;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += acc[mt][j][i];
@@ -222,11 +247,11 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
 // 32 bytes apart in the banks) and read transposed (ds_read_b64_tr_b16: 16
 // lanes addressing rows r0 + L / 4 and columns 4 (L % 4) .. + 3 receive rows
 // r0 .. r0 + 3 of column L); the dL operands are split once, by wave nt for
-// experts 16 nt .. + 16, and shared through LDS.  LDS reads are the bound, and
-// a dL block is three times an x block, so with 64 experts two waves share the
-// columns and a wave's tile is 128 columns by 32 experts (32 by 64: 50 us at
-// T = 16384, d = 4096, E = 64).  Two buffers, and the loads of the next PD
-// tiles in flight.
+// experts 16 nt .. + 16, and shared through LDS.  LDS reads and the tiles'
+// latency bound it, and a dL block is three times an x block, so with 64
+// experts two waves share the columns and a wave's tile is 128 columns by 32
+// experts (44 us at T = 16384, d = 4096, E = 64; 32 by 64: 50 us).  Two
+// buffers, and the loads of the next PD tiles in flight.
 template <bool BF, int NT, int CT>
 __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict__ dL, const void* __restrict__ x,
                                                         float* __restrict__ part, int T, int d, int E, int rows) {

@@ -4,12 +4,11 @@
 // Forward, per token row of d values:
 //   s = x + r (r the residual; none: s = x),  rstd = (mean(s^2) + eps)^(-1/2),
 //   y = s rstd w.
-// Sums, statistics and products are float32; s and y are each rounded once,
-// where they are stored, and y is computed from the unrounded s.  For MXFP8
-// blocks the row's E4M3 codes and E8M0 scales are written in the same pass.
-// They are the codes of the stored bf16 y (the arithmetic of
+// The squares are summed in float64; s and y are each rounded once, where they
+// are stored, and y is computed from the unrounded s.  For MXFP8 blocks the
+// row's E4M3 codes and E8M0 scales are written in the same pass.  They are the codes of the stored bf16 y (the arithmetic of
 // quantize_mxfp8_kernel), so an MXFP8 forward fed with them is bit for bit the
-// forward fed with y; the extra rounding is half a bf16 step, 2^-9 of a value,
+// forward fed with y; the extra rounding is half a bf16 step, 2^-8 of a value,
 // against the 2^-4 of the E4M3 rounding that follows.
 //
 // Backward, with n = s rstd and u = dy w:
@@ -52,8 +51,8 @@ __device__ __forceinline__ u32x4 pack16(const float (&v)[8]) {
 
 // Sum over the TPR threads of a row, the same on each (fixed order: butterfly
 // in the wave, then the waves in order).
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+template <int TPR, typename V>
+__device__ __forceinline__ V row_sum(V v, V* red) {
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
     if constexpr (TPR > 64) {
@@ -93,7 +92,8 @@ struct NormArgs {
     uint32_t* qs;        // with q: scale dwords [T][d / 128]
     float* rstd;         // optional
     int T, chunks;       // 16-byte chunks of a row
-    float inv_d, eps;
+    double inv_d;
+    float eps;
 };
 
 // TPR threads per row (a wave, or a workgroup of 256); CH chunks per thread
@@ -103,7 +103,7 @@ struct NormArgs {
 template <bool BF, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     constexpr int NV = BF ? 8 : 4;
-    __shared__ float red[4];
+    __shared__ double red[4];
     const int lt = threadIdx.x % TPR;
     const int t = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
     if (t >= a.T) return;   // whole waves (TPR 64), or never (one row per workgroup)
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         xr[g] = stream_load<NT>(a.x + row + c);
         if (a.r) rr[g] = stream_load<NT>(a.r + row + c);
     }
-    float ss = 0.f;
+    double ss = 0.0;
 #pragma unroll
     for (int g = 0; g < CH; ++g) {
         unpack16<BF>(xr[g], v[g]);
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         }
         if (lt + TPR * g < a.chunks) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) ss = fmaf(v[g][i], v[g][i], ss);
+            for (int i = 0; i < NV; ++i) ss = fma((double)v[g][i], (double)v[g][i], ss);
         }
     }
     auto load_sum = [&](int c, float (&o)[8]) {
@@ -144,16 +144,27 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         float o[8];
         load_sum(c, o);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) ss = fmaf(o[i], o[i], ss);
+        for (int i = 0; i < NV; ++i) ss = fma((double)o[i], (double)o[i], ss);
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(ss, red) * a.inv_d + a.eps);
+    // rstd as two floats (one step of Newton's method from the rounded root), and y from them and the two halves of
+    // s w: y is the float32 nearest to the exact value, so that a code or a scale at a rounding border is the exact
+    // value's too.  Three more operations a value than s rstd w, hidden behind the loads (94 us either way).
+    const double ms = row_sum<TPR>(ss, red) * a.inv_d + a.eps;
+    const float mh = (float)ms, ml = (float)(ms - mh);
+    const float r0 = 1.0f / sqrtf(mh), r2 = r0 * r0;
+    const float re = fmaf(-mh, r2, 1.0f) - fmaf(mh, fmaf(r0, r0, -r2), ml * r2);
+    const float corr = fabsf(re) < 1e-5f ? 0.5f * r0 * re : 0.f;   // 0: a square or root out of float32's range
+    const float rstd = r0 + corr, rl = corr != 0.f ? (r0 - rstd) + corr : 0.f;
     if (a.rstd && lt == 0) a.rstd[t] = rstd;
     auto emit = [&](int c, const float (&s)[8]) {
         if (a.sum) stream_store<NT>(a.sum + row + c, pack16<BF>(s));
         float wv[8], o[8];
         unpack16<BF>(a.w[c], wv);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) o[i] = s[i] * rstd * wv[i];
+        for (int i = 0; i < NV; ++i) {
+            const float p = s[i] * wv[i];
+            o[i] = fmaf(p, rstd, fmaf(p, rl, fmaf(s[i], wv[i], -p) * rstd));
+        }
         const u32x4 yp = pack16<BF>(o);
         if (a.y) stream_store<NT>(a.y + row + c, yp);
         if constexpr (BF) {
@@ -445,7 +456,7 @@ hipError_t launch_norm(int act, const void* x, const void* residual, const void*
     const NormArgs a{static_cast<const u32x4*>(x), static_cast<const u32x4*>(residual),
                      static_cast<const u32x4*>(weight), static_cast<u32x4*>(sum), static_cast<u32x4*>(y),
                      static_cast<uint2*>(q), reinterpret_cast<uint32_t*>(q_scale), rstd, T, d / (bf ? 8 : 4),
-                     1.0f / (float)d, eps};
+                     1.0 / d, eps};
     const bool nt = past_caches(T, a.chunks);
     if (bf && nt) launch_norm_t<true, true>(a, s);
     else if (bf) launch_norm_t<true, false>(a, s);

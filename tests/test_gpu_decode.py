@@ -88,6 +88,32 @@ def test_experts(T, d, E, k, H):
     assert torch.equal(alone[0], first[t])
 
 
+# enough experts in use for workgroups whose waves take weight rows of their own (up: E H / 64 >= 512 and more rows than
+# experts; down: the groups times d / 128 >= 512), with fewer slices than quarters, odd counts of them, and one expert
+# of up to 16, 32 and more rows
+@pytest.mark.parametrize("T, d, E, k, H", [(40, 128, 128, 4, 256), (40, 512, 128, 4, 128), (14, 640, 128, 10, 384),
+                                           (31, 1152, 72, 3, 512), (100, 384, 200, 2, 256), (11, 1024, 65, 6, 128),
+                                           (16, 4096, 20, 1, 128)])
+def test_experts_waves_side_by_side(T, d, E, k, H):
+    print(f"[decode wide] T={T} d={d} E={E} k={k} H={H}", flush=True)
+    rng, p, w, packed, x, idx, gate = _setup(T, d, E, k, H, seed=2)
+    for t in range(T):                                        # expert 3 in a slot of every token but the last
+        if t < T - 1 and 3 not in idx[t]:
+            idx[t, t % k] = 3
+    idx[1, 0] = -1
+    dec = B.Decode(p, DEV)
+    dec.ws.fill_(255)
+    args = [torch.from_numpy(idx).to(DEV), torch.from_numpy(gate).to(DEV), packed]
+    y = dec.experts(x.to(DEV), *args).clone()
+    for _ in range(3):
+        assert torch.equal(dec.experts(x.to(DEV), *args), y)
+    _expect(y, x, idx, np.where(idx >= 0, gate, 0).astype(np.float32), packed, E, d, H)
+    one = B.Decode(B.problem(1, d, E, k, H, "bf16"), DEV)
+    for t in (0, T - 1):
+        alone = one.experts(x[t:t + 1].to(DEV), *(a[t:t + 1] for a in args[:2]), packed)
+        assert torch.equal(alone[0], y[t])
+
+
 @pytest.mark.parametrize("T, E", [(6, 40), (40, 6)])
 def test_unused_slots_repeated_experts_and_nonfinite_rows(T, E):
     d, k, H = 256, 3, 128

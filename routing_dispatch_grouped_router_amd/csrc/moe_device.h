@@ -120,4 +120,16 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)pk;
 }
 
+// 16 bytes of a stream; NT: past the caches, for tensors that they cannot hold
+// for whoever reads them next.
+template <bool NT>
+__device__ __forceinline__ u32x4 stream_load(const u32x4* p) {
+    return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT>
+__device__ __forceinline__ void stream_store(u32x4* p, const u32x4& v) {
+    if (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 }  // namespace moe

@@ -231,6 +231,12 @@ hipError_t launch_gemm_plain(int act, const void* A, const void* B, void* C, con
 hipError_t launch_wgrad_rows(int omap, const uint16_t* XA, const uint16_t* XB, const int32_t* offsets, int E, int M,
                              int N, float* C, float* C2, hipStream_t s);
 
+// Whether a tensor is to be streamed past the caches: as large as the eight 4 MB
+// L2s together.  The norm, T = 16384, d = 4096, bf16: 94 us through the caches,
+// 89 past them; T = 32768, d = 2048, MXFP8 with codes: 105 and 94; T = 2048,
+// d = 4096 (17 MB): 11.0 and 13.3.
+inline bool past_caches(size_t bytes) { return bytes >= (size_t)32 << 20; }
+
 // ---------------------------------------------------------------- norm (norm.hip)
 
 // Per row: s = x + residual, rstd = (mean s^2 + eps)^-1/2, y = s rstd weight.  residual, sum, y,

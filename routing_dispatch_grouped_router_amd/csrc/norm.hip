@@ -65,23 +65,6 @@ __device__ __forceinline__ V row_sum(V v, V* red) {
     return v;
 }
 
-// 16 bytes of a stream; NT: past the caches, for tensors that they cannot hold
-// for whoever reads them next.
-template <bool NT>
-__device__ __forceinline__ u32x4 stream_load(const u32x4* p) {
-    return NT ? __builtin_nontemporal_load(p) : *p;
-}
-template <bool NT>
-__device__ __forceinline__ void stream_store(u32x4* p, const u32x4& v) {
-    if (NT) __builtin_nontemporal_store(v, p);
-    else *p = v;
-}
-
-// A tensor as large as the eight 4 MB L2s together.  Forward, T = 16384,
-// d = 4096, bf16: 94 us through the caches, 89 past them; T = 32768, d = 2048,
-// MXFP8 with codes: 105 and 94; T = 2048, d = 4096 (17 MB): 11.0 and 13.3.
-bool past_caches(int T, int chunks) { return (size_t)T * chunks * 16 >= (size_t)32 << 20; }
-
 struct NormArgs {
     const u32x4* x;
     const u32x4* r;      // NULL: no residual
@@ -441,7 +424,7 @@ void launch_norm_bwd_t(const NormBwdArgs& a, const NormBwdPlan& p, hipStream_t s
     if (p.tpr == 0) {
         hipLaunchKernelGGL((norm_bwd_long_kernel<BF>), dim3(a.T), dim3(256), 0, s, a);
         hipLaunchKernelGGL((norm_dweight_long_kernel<BF>), dim3((a.chunks + 255) / 256, p.blocks), dim3(256), 0, s, a);
-    } else if (past_caches(a.T, a.chunks)) {   // (T = 8000, d = 512, 8 MB: 11.3 us through them, 12.4 past them)
+    } else if (past_caches((size_t)a.T * a.chunks * 16)) {   // (T = 8000, d = 512, 8 MB: 11.3 us through them, 12.4 past them)
         launch_norm_bwd_rows<BF, true>(a, p, s);
     } else {
         launch_norm_bwd_rows<BF, false>(a, p, s);
@@ -457,7 +440,7 @@ hipError_t launch_norm(int act, const void* x, const void* residual, const void*
                      static_cast<const u32x4*>(weight), static_cast<u32x4*>(sum), static_cast<u32x4*>(y),
                      static_cast<uint2*>(q), reinterpret_cast<uint32_t*>(q_scale), rstd, T, d / (bf ? 8 : 4),
                      1.0 / d, eps};
-    const bool nt = past_caches(T, a.chunks);
+    const bool nt = past_caches((size_t)T * a.chunks * 16);
     if (bf && nt) launch_norm_t<true, true>(a, s);
     else if (bf) launch_norm_t<true, false>(a, s);
     else if (nt) launch_norm_t<false, true>(a, s);

@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_terms_full(const void* p, uint32_t i, bf16x
 // block j is column 8 n + j, so that a lane's eight blocks hold 8 consecutive
 // columns of a token and sixteen lanes 128: add is read and dx written in whole
 // lines (a lane layout with a row per lane cost the memory pipe an access per
-// lane, 126 us at T = 16384, d = 4096, E = 64; 75 us so, 3.6 TB/s).  Both operands pass through LDS
+// lane, 126 us at T = 16384, d = 4096, E = 64; 73 us so).  Both operands pass through LDS
 // in fragment order, 32 experts at a time, loaded in whole 64- and 128-byte
 // pieces and split once for the workgroup; two buffers, the next experts' loads
 // in flight during a step's products.  `add`: row t of add (pos NULL; requested
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
     // thread: experts 8 (tid % 4) .. of token tid / 4 and of columns tid / 4 + 64 i
     const int lr = tid >> 2, lq = tid & 3;
     // (uniform bases and 32-bit lane offsets, and a path without the test for the last expert: address and select
-    // instructions held this kernel up, 79 us with a 64-bit offset and a test a load at the size above, 75 us so)
+    // instructions held this kernel up, 79 us with a 64-bit offset and a test a load at the size above, 73 us so)
     const float* dl0 = dL + (size_t)t0 * E;
     const char* w0 = static_cast<const char*>(w) + (size_t)c0 * E * (BF ? 2 : 4);
     const uint32_t dlo = (uint32_t)min(lr, T - 1 - t0) * (uint32_t)E + 8 * lq;
@@ -239,6 +239,125 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
                 dst[t * row_chunks + cb + g] = o;
             }
         }
+}
+
+// The same for bfloat16 blocks of at most 32 NS experts (two 32's fit the LDS
+// of two workgroups) and rows added one for one: a workgroup keeps its 256
+// columns of W_r in LDS and walks `rows` tokens, 64 at a time, the next tokens'
+// dL and rows of add in flight during a tile's products.  64 us at T = 16384,
+// d = 4096, E = 64, 4.2 TB/s, of it 2 us by passing the caches (the kernel
+// above: 73); 15 us at T = 8192, d = 2048, E = 8 (17).
+template <int NS, bool NT>
+__global__ __launch_bounds__(256) void router_dx_resident_kernel(const float* __restrict__ dL,
+                                                                 const uint16_t* __restrict__ w, const u32x4* add,
+                                                                 u32x4* dx, int T, int d, int E, int rows) {
+    __shared__ u32x4 s_w[NS][16][64];
+    __shared__ u32x4 s_a[2][NS][4][3][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
+    const int ncb = (d + 255) / 256, tb = blockIdx.x / ncb, c0 = (int)(blockIdx.x - tb * ncb) * 256;
+    const int ta = tb * rows, te = min(T, ta + rows);
+    const int wc = c0 + 128 * (wave >> 1), lr = tid >> 2, lq = tid & 3;
+    const bool vec = (E & 7) == 0, in_cols = wc + 8 * m < d;
+    const uint32_t row_chunks = (uint32_t)d / 8, cb = (uint32_t)(wc + 8 * m) / 8;
+    f32x4 la[NS][2];
+    auto load_dl = [&](int t0) {
+        const float* base = dL + (size_t)t0 * E;
+        const uint32_t o = (uint32_t)min(lr, te - 1 - t0) * (uint32_t)E + 8 * lq;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const int n = E - 32 * s - 8 * lq;
+            if (vec) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    la[s][g] = n > 0 ? *reinterpret_cast<const f32x4*>(base + (o + 32 * s + 4 * g)) : (f32x4){0.f, 0.f, 0.f, 0.f};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) la[s][j / 4][j % 4] = j < n ? base[o + 32 * s + j] : 0.f;
+            }
+        }
+    };
+    u32x4 base[2][4];
+    auto load_base = [&](int t0) {
+        const u32x4* at = add + (size_t)t0 * row_chunks;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = min(32 * (wave & 1) + 16 * mt + 4 * q + i, te - 1 - t0);
+                base[mt][i] = stream_load<NT>(at + ((uint32_t)t * row_chunks + (in_cols ? cb : 0u)));
+            }
+    };
+    load_dl(ta);
+    {
+        const uint16_t* w0 = w + (size_t)c0 * E;
+        bf16x8 rw[NS][4][1];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_terms<true>(w0 + 32 * s, (size_t)min(lr + 64 * i, d - 1 - c0) * E + 8 * lq, E - 32 * s - 8 * lq, vec,
+                                 rw[s][i]);
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = lr + 64 * i, j = c & 7, n = (c >> 3) & 15;
+                s_w[s][8 * (c >> 7) + j][16 * lq + (n ^ (4 * lq) ^ (j & 3))] = __builtin_bit_cast(u32x4, rw[s][i][0]);
+            }
+    }
+    if (add) load_base(ta);
+    int buf = 0;
+    for (int t0 = ta; t0 < te; t0 += 64, buf ^= 1) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const float v[8] = {la[s][0][0], la[s][0][1], la[s][0][2], la[s][0][3],
+                                la[s][1][0], la[s][1][1], la[s][1][2], la[s][1][3]};
+            bf16x8 o[3];
+            split3(v, o);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                s_a[buf][s][lr >> 4][p][16 * lq + ((lr & 15) ^ (4 * lq))] = __builtin_bit_cast(u32x4, o[p]);
+        }
+        __syncthreads();   // also: every wave has left the buffer that is written next
+        if (t0 + 64 < te) load_dl(t0 + 64);
+        f32x4 acc[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            bf16x8 a[2][3];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    a[mt][p] = __builtin_bit_cast(bf16x8, s_a[buf][s][2 * (wave & 1) + mt][p][16 * q + (m ^ (4 * q))]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bf16x8 b[1] = {
+                    __builtin_bit_cast(bf16x8, s_w[s][8 * (wave >> 1) + j][16 * q + (m ^ (4 * q) ^ (j & 3))])};
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) acc[mt][j] = mfma_terms<3, 1>(a[mt], b, acc[mt][j]);
+            }
+        }
+        u32x4* dt = dx + (size_t)t0 * row_chunks;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 32 * (wave & 1) + 16 * mt + 4 * q + i;
+                u32x4 o;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t c = add ? base[mt][i][h] : 0u;
+                    o[h] = pack_bf16x2(__uint_as_float(c << 16) + acc[mt][2 * h][i],
+                                       __uint_as_float(c & 0xFFFF0000u) + acc[mt][2 * h + 1][i]);
+                }
+                if (in_cols && t0 + t < te) stream_store<NT>(dt + ((uint32_t)t * row_chunks + cb), o);
+            }
+        if (add && t0 + 64 < te) load_base(t0 + 64);
+    }
 }
 
 // dW_r partials: a workgroup sums CT columns x 16 NT experts over a range of
@@ -437,9 +556,27 @@ void launch_router_dw_t(const float* dL, const void* x, float* dst, const Router
 
 }  // namespace
 
+// Workgroups of the resident kernel: two rounds of the two that a compute unit
+// holds (T = 16384, d = 4096, E = 64 and T = 8192, d = 2048, E = 8: 512 of them
+// 67 and 19 us, 1024 66 and 16, 2048 68 and 16).
+constexpr int kDxGroups = 1024;
+
 hipError_t launch_router_dx(int act, const float* dL, const void* w_router, const void* add, const int32_t* pos, int k,
                             void* dx, int T, int d, int E, hipStream_t s) {
-    const dim3 g((T + 63) / 64 * ((d + 255) / 256)), b(256);
+    const int ncb = (d + 255) / 256;
+    if (act != kF32 && !pos && E <= 64) {
+        const int ranges = std::max(1, kDxGroups / ncb), rows = std::max(1, ((T + ranges - 1) / ranges + 63) / 64) * 64;
+        const dim3 g((T + rows - 1) / rows * ncb), b(256);
+        const uint16_t* w = static_cast<const uint16_t*>(w_router);
+        const u32x4* in = static_cast<const u32x4*>(add);
+        u32x4* out = static_cast<u32x4*>(dx);
+        const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, 0, s, dL, w, in, out, T, d, E, rows); };
+        const bool nt = past_caches((size_t)T * d * 2);
+        if (E <= 32) nt ? go(router_dx_resident_kernel<1, true>) : go(router_dx_resident_kernel<1, false>);
+        else nt ? go(router_dx_resident_kernel<2, true>) : go(router_dx_resident_kernel<2, false>);
+        return hipGetLastError();
+    }
+    const dim3 g((T + 63) / 64 * ncb), b(256);
     if (act == kF32)
         hipLaunchKernelGGL((router_dx_kernel<false>), g, b, 0, s, dL, w_router, add, pos, k, dx, T, d, E);
     else

@@ -132,3 +132,27 @@ def test_router_backward(T, d, E, act, add):
     if add:   # in place
         op.dx = add_dev
         assert torch.equal(op(*dev, dx_in=add_dev)["dx"], first["dx"])
+
+
+@pytest.mark.parametrize("T, d, E", [(70001, 64, 20), (33100, 320, 33), (262300, 64, 9), (131100, 128, 64)])
+@pytest.mark.parametrize("add", [False, True])
+def test_router_backward_many_tokens(T, d, E, add):
+    """Several tiles of tokens for a workgroup, the last of them short, and rows past 32 MB."""
+    print(f"[router backward] T={T} d={d} E={E} add={add}", flush=True)
+    g = torch.Generator().manual_seed(T)
+    dl = torch.randn(T, E, generator=g)
+    x, w, a = (torch.randn(*s, generator=g).to(torch.bfloat16) for s in ((T, d), (d, E), (T, d)))
+    op = B.RouterBackward(B.problem(T, d, E, 1, 64, "bf16"), DEV)
+    dev = [t.to(DEV) for t in (dl, x, w)]
+    add_dev = a.to(DEV) if add else None
+    first = {k: v.clone() for k, v in op(*dev, dx_in=add_dev).items()}
+    dl64, x64, w64, a64 = (as_f64(t) for t in (dl, x, w, a))
+    ref = dl64 @ w64.T + (a64 if add else 0)
+    mag = np.abs(dl64) @ np.abs(w64).T + (np.abs(a64) if add else 0)
+    _close("dx", first["dx"], ref, 2.0 ** -8 * np.abs(ref) + (6 * E + 16) * U * mag)
+    # up to 512 ranges of T / 512 rows (rounded up by less than 160), added after
+    _close("dw_router", first["dw_router"], x64.T @ dl64,
+           (6 * (T / 512 + 160) + 512 + 64) * U * (np.abs(x64).T @ np.abs(dl64)))
+    if add:   # in place
+        op.dx = add_dev
+        assert torch.equal(op(*dev, dx_in=add_dev)["dx"], first["dx"])

@@ -17,13 +17,17 @@
 // value and the rounded remainder, 2^-16 of it left out): rounded once it would
 // add as much error to y as y's own rounding, and the second term costs loads
 // that hit the caches and matrix instructions that the weights' bytes hide.
-// Rows are not sorted or moved: a workgroup
-// finds its expert's rows in topk_idx itself, and an index outside [0, E) is a
-// slot not in use.
+// Rows are not sorted or moved: a workgroup finds its expert's rows in topk_idx
+// itself, and an index outside [0, E) is a slot not in use.
 //
 // Every sum over K is taken in four quarters (of K / 128 slices, in order) that
 // are added in order, whichever kernel and however many rows: a token's result
 // does not depend on the tokens beside it.
+//
+// The weights' bytes bound it.  d = 4096, E = 64, k = 8, H = 1536: one token 20 us
+// (80 MB, 4.0 TB/s), 64 tokens 145 us (643 MB, 4.4 TB/s); T = 7, d = 2048, E = 128,
+// k = 4, H = 1024: 20 us (63 MB, 3.1 TB/s; two launches of 2.5 us and more whatever
+// they read).  A 2 GiB copy runs at 4.9 TB/s on the same card.
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -702,6 +706,15 @@ hipError_t launch_pack_mxfp4(const void* w_gate, const void* w_up, const void* w
 // and 2048 of them): 152 us against 169 with the waves on the quarters of K,
 // T = 256: 273 and 359; T = 16, E = 8, k = 2, H = 1536 (192 and 256): 18.4 + 10.5
 // us the two products against 13.2 + 9.3.
+// With no more rows than experts a group mostly holds one row, few activations
+// to share: the up projection then keeps its waves on the quarters (T = 12,
+// d = 4096, E = 64, k = 4, H = 1536: 46 us against 55); the down projection, with
+// two terms of h and a short K, does not (34 against 31).
+// Up to half as many rows as experts a token's workgroup joins its own slots,
+// which saves ye and a launch and reads shared experts again: T = 1, k = 8: 8.3
+// us against 9.0 + 3.9, T = 4: 27 against 25 + 5, T = 6 (48 rows): 41 against
+// 31 + 5.  It takes 16 outputs rather than 32 where 32 give fewer workgroups
+// than compute units: T = 1: 8.3 us against 11.6, T = 2: 16.0 against 14.1.
 constexpr int kWideGroups = 512;
 
 hipError_t launch_decode_experts(const uint16_t* x, const int32_t* idx, const float* gate, const uint8_t* w1,

@@ -81,8 +81,9 @@ struct NormArgs {
 
 // TPR threads per row (a wave, or a workgroup of 256); CH chunks per thread
 // stay in registers, chunks past TPR CH of a longer row are read again.  A wave
-// takes rows of up to two chunks a lane: with eight (4096 bf16 values) the
-// registers leave too few waves to cover the loads (103 us against 94).
+// takes rows of up to two chunks a lane (T = 8000, d = 1024, bf16: 10.9 us, a
+// workgroup a row 14.5); with four (T = 32768, d = 2048: 97 us against 93) or
+// eight (T = 16384, d = 4096: 103 against 94) too few waves cover the loads.
 template <bool BF, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     constexpr int NV = BF ? 8 : 4;
@@ -399,7 +400,7 @@ template <bool BF, bool NT>
 void launch_norm_t(const NormArgs& a, hipStream_t s) {
     const dim3 b(256), rows(a.T), waves((a.T + 3) / 4);
     if (a.chunks <= 64) hipLaunchKernelGGL((norm_kernel<BF, 64, 1, NT>), waves, b, 0, s, a);
-    else if (a.chunks <= 128 && a.T >= 1024) hipLaunchKernelGGL((norm_kernel<BF, 64, 2, NT>), waves, b, 0, s, a);
+    else if (a.chunks <= 128) hipLaunchKernelGGL((norm_kernel<BF, 64, 2, NT>), waves, b, 0, s, a);
     else if (a.chunks <= 256) hipLaunchKernelGGL((norm_kernel<BF, 256, 1, NT>), rows, b, 0, s, a);
     else if (a.chunks <= 512) hipLaunchKernelGGL((norm_kernel<BF, 256, 2, NT>), rows, b, 0, s, a);
     else hipLaunchKernelGGL((norm_kernel<BF, 256, 4, NT>), rows, b, 0, s, a);
@@ -422,8 +423,9 @@ void launch_norm_bwd_rows(const NormBwdArgs& a, const NormBwdPlan& p, hipStream_
 template <bool BF>
 void launch_norm_bwd_t(const NormBwdArgs& a, const NormBwdPlan& p, hipStream_t s) {
     if (p.tpr == 0) {
-        hipLaunchKernelGGL((norm_bwd_long_kernel<BF>), dim3(a.T), dim3(256), 0, s, a);
+        // the weight gradient first: ds may be dy
         hipLaunchKernelGGL((norm_dweight_long_kernel<BF>), dim3((a.chunks + 255) / 256, p.blocks), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((norm_bwd_long_kernel<BF>), dim3(a.T), dim3(256), 0, s, a);
     } else if (past_caches((size_t)a.T * a.chunks * 16)) {   // (T = 8000, d = 512, 8 MB: 11.3 us through them, 12.4 past them)
         launch_norm_bwd_rows<BF, true>(a, p, s);
     } else {

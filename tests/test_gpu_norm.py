@@ -138,8 +138,9 @@ def test_norm_backward(T, d, act, dsum):
     _close("dweight", g["dweight"], dw_ref, 80 * U * (np.abs(dy64) * n).sum(0))
 
 
-def test_norm_backward_in_place():
-    T, d = 500, 256
+# a wave's rows, a workgroup's rows past the caches, rows read twice
+@pytest.mark.parametrize("T, d", [(500, 256), (4200, 4096), (40, 8448)])
+def test_norm_backward_in_place(T, d):
     rng = np.random.default_rng(5)
     s, dy, e, w = (_rand(rng, sh, "bf16").to(DEV) for sh in ((T, d), (T, d), (T, d), (d,)))
     rstd = (s.float().square().mean(1) + 1e-6).rsqrt()

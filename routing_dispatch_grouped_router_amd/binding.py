@@ -142,11 +142,11 @@ def _own(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, device=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -180,10 +180,47 @@ def _bytes(fn: str, p: Problem) -> int:
     return n.value
 
 
-def _on_current(t, name="x"):
-    """The kernels run on the current device, on the given stream of it."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _inputs(device, *tensors):
+    """Addresses of a call's inputs: contiguous tensors (or None) on the current
+    device, `device`, on whose given stream the kernels run."""
+    ptrs = []
+    for t in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a device tensor")
+        if t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, expected cuda:{device}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        ptrs.append(t.data_ptr())
+    if torch.cuda.current_device() != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    return ptrs
+
+
+class _Operator:
+    """An operator's problem (a copy: its buffers are of that size) and buffers.
+    Another tensor may be put in a buffer's place (an output over an input, say),
+    of the same shape and type; an optional one may be None."""
+
+    def __init__(self, p: Problem, device):
+        self.p = Problem.from_buffer_copy(p)
+        self._p, self._device, self._specs = ctypes.byref(self.p), torch.device(device), {}
+        self._index = -1 if self._device.type != "cuda" else (
+            torch.cuda.current_device() if self._device.index is None else self._device.index)
+
+    def _buffer(self, name, shape, dtype, wanted=True):
+        self._specs[name] = shape, dtype
+        self.__dict__[name] = torch.empty(shape, dtype=dtype, device=self._device) if wanted else None
+
+    def __setattr__(self, name, value):
+        if value is not None and name in self.__dict__.get("_specs", ()):
+            _expect(value, *self._specs[name], name)
+            if _ptr(value) is not None and value.get_device() != self._index:
+                raise ValueError(f"{name} is on {value.device}, expected cuda:{self._index}")
+        object.__setattr__(self, name, value)
 
 
 # ----------------------------------------------------------------------------- host-only queries
@@ -464,22 +501,22 @@ class Backward:
                     dw_down=self.dw_down, dw_router=self.dw_router)
 
 
-class Norm:
+class Norm(_Operator):
     """Preallocated outputs of moe_norm: y [T, d], rstd [T], with a residual its
     sum [T, d], for MXFP8 problems the rows' codes q [T, d] and scales q_scale
     [T, d/32] (uint8) unless quantized is False."""
 
     def __init__(self, p: Problem, device, eps: float = 1e-6, residual: bool = True, quantized: bool | None = None):
-        self.p, self.eps = p, float(eps)
-        self._p = ctypes.byref(p)
+        super().__init__(p, device)
+        self.eps = float(eps)
         (T, d), dt = self._shape, self._dt = _rows(p)
         if quantized is None:
             quantized = p.act == "mxfp8"
-        self.y = torch.empty((T, d), dtype=dt, device=device)
-        self.sum = torch.empty((T, d), dtype=dt, device=device) if residual else None
-        self.rstd = torch.empty((T,), dtype=torch.float32, device=device)
-        self.q = torch.empty((T, d), dtype=torch.uint8, device=device) if quantized else None
-        self.q_scale = torch.empty((T, d // 32), dtype=torch.uint8, device=device) if quantized else None
+        self._buffer("y", (T, d), dt)
+        self._buffer("sum", (T, d), dt, residual)
+        self._buffer("rstd", (T,), torch.float32)
+        self._buffer("q", (T, d), torch.uint8, quantized)
+        self._buffer("q_scale", (T, d // 32), torch.uint8, quantized)
 
     def __call__(self, x, weight, residual=None, stream=None):
         """y = norm(x + residual) weight; returns y."""
@@ -490,22 +527,21 @@ class Norm:
             raise ValueError("residual: " + ("expected" if residual is None else "not expected"))
         if residual is not None:
             _expect(residual, shape, dt, "residual")
-        _on_current(x)
         _check("moe_norm", lib().moe_norm(
-            self._p, _ptr(x), _ptr(residual), _ptr(weight), self.eps, _own(self.sum), _own(self.y),
-            _own(self.q), _own(self.q_scale), _own(self.rstd), _stream(stream)))
+            self._p, *_inputs(self._index, x, residual, weight), self.eps, _own(self.sum), _own(self.y),
+            _own(self.q), _own(self.q_scale), _own(self.rstd), _stream(stream, self._index)))
         return self.y
 
 
-class NormBackward:
+class NormBackward(_Operator):
     """Preallocated gradients and workspace of moe_norm_backward."""
 
     def __init__(self, p: Problem, device):
-        self.p, self._p = p, ctypes.byref(p)
+        super().__init__(p, device)
         self._shape, self._dt = _rows(p)
-        self.ws = torch.empty(_bytes("moe_norm_backward_workspace_bytes", p), dtype=torch.uint8, device=device)
-        self.ds = torch.empty(self._shape, dtype=self._dt, device=device)
-        self.dweight = torch.empty((p.d_model,), dtype=torch.float32, device=device)
+        self._buffer("ws", (_bytes("moe_norm_backward_workspace_bytes", p),), torch.uint8)
+        self._buffer("ds", self._shape, self._dt)
+        self._buffer("dweight", (p.d_model,), torch.float32)
 
     def __call__(self, dy, s, weight, rstd, dsum=None, stream=None) -> dict:
         """dy: the gradient of y; s: the forward's sum (x without a residual); dsum: the
@@ -517,61 +553,60 @@ class NormBackward:
         _expect(rstd, shape[:1], torch.float32, "rstd")
         if dsum is not None:
             _expect(dsum, shape, dt, "dsum")
-        _on_current(dy, "dy")
         _check("moe_norm_backward", lib().moe_norm_backward(
-            self._p, _ptr(dy), _ptr(dsum), _ptr(s), _ptr(weight), _ptr(rstd), _own(self.ds),
-            _own(self.dweight), _own(self.ws), self.ws.numel(), _stream(stream)))
+            self._p, *_inputs(self._index, dy, dsum, s, weight, rstd), _own(self.ds),
+            _own(self.dweight), _own(self.ws), self.ws.numel(), _stream(stream, self._index)))
         return dict(ds=self.ds, dweight=self.dweight)
 
 
-class BalanceLoss:
+class BalanceLoss(_Operator):
     """Preallocated outputs and workspace of moe_balance_loss and its backward:
     loss [2] (balance, z), counts [E], live [1] (tokens), dlogits [T, E]."""
 
     def __init__(self, p: Problem, device):
-        self.p, self._p = p, ctypes.byref(p)
+        super().__init__(p, device)
         self._shape, self._choices = (p.T, p.n_experts), (p.T, p.top_k)
-        self.ws = torch.empty(_bytes("moe_balance_workspace_bytes", p), dtype=torch.uint8, device=device)
-        self.loss = torch.empty((2,), dtype=torch.float32, device=device)
-        self.counts_live = torch.empty((p.n_experts + 1,), dtype=torch.int32, device=device)
+        self._buffer("ws", (_bytes("moe_balance_workspace_bytes", p),), torch.uint8)
+        self._buffer("loss", (2,), torch.float32)
+        self._buffer("counts_live", (p.n_experts + 1,), torch.int32)
         self.counts, self.live = self.counts_live[:-1], self.counts_live[-1:]
-        self.dlogits = torch.empty((p.T, p.n_experts), dtype=torch.float32, device=device)
+        self._buffer("dlogits", self._shape, torch.float32)
 
     def _expect_logits(self, logits, mask):
         _expect(logits, self._shape, torch.float32, "logits")
         if mask is not None:
             _expect(mask, self._shape[:1], torch.uint8, "mask")
-        _on_current(logits, "logits")
 
     def __call__(self, logits, idx, mask=None, stream=None):
         """loss [2] of the tokens whose mask (uint8 [T]; None: all) is not zero."""
         self._expect_logits(logits, mask)
         _expect(idx, self._choices, torch.int32, "idx")
         _check("moe_balance_loss", lib().moe_balance_loss(
-            self._p, _ptr(logits), _ptr(idx), _ptr(mask), _own(self.counts_live), _own(self.loss),
-            _own(self.ws), self.ws.numel(), _stream(stream)))
+            self._p, *_inputs(self._index, logits, idx, mask), _own(self.counts_live), _own(self.loss),
+            _own(self.ws), self.ws.numel(), _stream(stream, self._index)))
         return self.loss
 
     def backward(self, logits, dloss, mask=None, stream=None):
         """dlogits for dloss [2], with the counts of the last call."""
         self._expect_logits(logits, mask)
         _expect(dloss, (2,), torch.float32, "dloss")
+        logits, mask, dloss = _inputs(self._index, logits, mask, dloss)
         _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-            self._p, _ptr(logits), _ptr(mask), _own(self.counts_live), _ptr(dloss), _own(self.dlogits),
-            _stream(stream)))
+            self._p, logits, mask, _own(self.counts_live), dloss, _own(self.dlogits),
+            _stream(stream, self._index)))
         return self.dlogits
 
 
-class RouterBackward:
+class RouterBackward(_Operator):
     """Preallocated gradients and workspace of moe_router_backward."""
 
     def __init__(self, p: Problem, device):
-        self.p, self._p = p, ctypes.byref(p)
+        super().__init__(p, device)
         self._shape, self._dt = _rows(p)
         self._logits, self._weight = (p.T, p.n_experts), (p.d_model, p.n_experts)
-        self.ws = torch.empty(_bytes("moe_router_backward_workspace_bytes", p), dtype=torch.uint8, device=device)
-        self.dx = torch.empty(self._shape, dtype=self._dt, device=device)
-        self.dw_router = torch.empty((p.d_model, p.n_experts), dtype=torch.float32, device=device)
+        self._buffer("ws", (_bytes("moe_router_backward_workspace_bytes", p),), torch.uint8)
+        self._buffer("dx", self._shape, self._dt)
+        self._buffer("dw_router", self._weight, torch.float32)
 
     def __call__(self, dlogits, x, w_router, dx_in=None, stream=None) -> dict:
         shape, dt = self._shape, self._dt
@@ -580,10 +615,9 @@ class RouterBackward:
         _expect(w_router, self._weight, dt, "w_router")
         if dx_in is not None:
             _expect(dx_in, shape, dt, "dx_in")
-        _on_current(x)
         _check("moe_router_backward", lib().moe_router_backward(
-            self._p, _ptr(dlogits), _ptr(x), _ptr(w_router), _ptr(dx_in), _own(self.dx), _own(self.dw_router),
-            _own(self.ws) if self.ws.numel() else None, self.ws.numel(), _stream(stream)))
+            self._p, *_inputs(self._index, dlogits, x, w_router, dx_in), _own(self.dx), _own(self.dw_router),
+            _own(self.ws) if self.ws.numel() else None, self.ws.numel(), _stream(stream, self._index)))
         return dict(dx=self.dx, dw_router=self.dw_router)
 
 
@@ -600,27 +634,27 @@ def pack_weights_decode(p: Problem, w_gate, w_up, w_down, stream=None) -> torch.
     _expect(w_gate, (E, d, H), torch.bfloat16, "w_gate")
     _expect(w_up, (E, d, H), torch.bfloat16, "w_up")
     _expect(w_down, (E, H, d), torch.bfloat16, "w_down")
-    _on_current(w_gate, "w_gate")
+    weights = _inputs(w_gate.get_device(), w_gate, w_up, w_down)
     packed = torch.empty(decode_weight_bytes(p), dtype=torch.uint8, device=w_gate.device)
     _check("moe_pack_weights_decode", lib().moe_pack_weights_decode(
-        ctypes.byref(p), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(packed), _stream(stream)))
+        ctypes.byref(p), *weights, packed.data_ptr(), _stream(stream)))
     return packed
 
 
-class Decode:
+class Decode(_Operator):
     """Preallocated output and workspace of the block for a few tokens with 4-bit
     weights (moe_decode, moe_decode_experts): y [T, d], logits [T, E], idx and
     gate [T, k]."""
 
     def __init__(self, p: Problem, device):
-        self.p, self._p = p, ctypes.byref(p)
+        super().__init__(p, device)
         self._shape, self._choices = (p.T, p.d_model), (p.T, p.top_k)
         self.weight_bytes = decode_weight_bytes(p)
-        self.ws = torch.empty(_bytes("moe_decode_workspace_bytes", p), dtype=torch.uint8, device=device)
-        self.y = torch.empty((p.T, p.d_model), dtype=torch.bfloat16, device=device)
-        self.logits = torch.empty((p.T, p.n_experts), dtype=torch.float32, device=device)
-        self.idx = torch.empty((p.T, p.top_k), dtype=torch.int32, device=device)
-        self.gate = torch.empty((p.T, p.top_k), dtype=torch.float32, device=device)
+        self._buffer("ws", (_bytes("moe_decode_workspace_bytes", p),), torch.uint8)
+        self._buffer("y", self._shape, torch.bfloat16)
+        self._buffer("logits", (p.T, p.n_experts), torch.float32)
+        self._buffer("idx", self._choices, torch.int32)
+        self._buffer("gate", self._choices, torch.float32)
 
     def __call__(self, x, packed, w_router=None, logits=None, stream=None):
         """The block: router logits (or given ones), top-k and gates, experts; returns y."""
@@ -632,10 +666,9 @@ class Decode:
         else:
             _expect(w_router, (p.d_model, p.n_experts), torch.bfloat16, "w_router")
             logits = self.logits
-        _on_current(x)
         _check("moe_decode", lib().moe_decode(
-            self._p, _ptr(x), _ptr(w_router), _ptr(logits), _ptr(packed), _own(self.y), _own(self.idx),
-            _own(self.gate), _own(self.ws), self.ws.numel(), _stream(stream)))
+            self._p, *_inputs(self._index, x, w_router, logits, packed), _own(self.y), _own(self.idx),
+            _own(self.gate), _own(self.ws), self.ws.numel(), _stream(stream, self._index)))
         return self.y
 
     def experts(self, x, idx, gate, packed, stream=None):
@@ -644,10 +677,9 @@ class Decode:
         _expect(idx, self._choices, torch.int32, "idx")
         _expect(gate, self._choices, torch.float32, "gate")
         _expect(packed, (self.weight_bytes,), torch.uint8, "packed")
-        _on_current(x)
         _check("moe_decode_experts", lib().moe_decode_experts(
-            self._p, _ptr(x), _ptr(idx), _ptr(gate), _ptr(packed), _own(self.y), _own(self.ws),
-            self.ws.numel(), _stream(stream)))
+            self._p, *_inputs(self._index, x, idx, gate, packed), _own(self.y), _own(self.ws),
+            self.ws.numel(), _stream(stream, self._index)))
         return self.y
 
 

@@ -205,3 +205,32 @@ def test_binding_checks_shapes_types_and_place():
     with pytest.raises(ValueError, match="xq_scale"):
         B.Forward(pm, "cpu")(None, logits=torch.zeros(4, 8), xq=torch.zeros(4, 256, dtype=torch.uint8),
                              xq_scale=torch.zeros(4, 4, dtype=torch.uint8))
+
+
+def test_operators_keep_their_problem_and_check_buffers_put_in_place():
+    p = _p(T=4)
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    w = torch.zeros(256, dtype=torch.bfloat16)
+    op = B.Norm(p, "cpu")
+    p.T = 4096                                                # another problem: the operator's stays
+    assert op.p.T == 4 and op.y.shape == (4, 256)
+    with pytest.raises(ValueError, match="device tensor"):
+        op(x, w, residual=x)
+    p.T = 4
+    for make, name in ((B.Norm, "y"), (B.Norm, "sum"), (B.NormBackward, "ds"), (B.BalanceLoss, "dlogits"),
+                       (B.RouterBackward, "dx"), (B.Decode, "y"), (B.Decode, "idx")):
+        op = make(p, "cpu")
+        own = getattr(op, name)
+        for wrong in (own[:2], own.double()):
+            with pytest.raises(ValueError, match=name):
+                setattr(op, name, wrong)
+        with pytest.raises(ValueError, match="device tensor"):
+            setattr(op, name, own.clone())
+        assert getattr(op, name) is own
+    op = B.Norm(p, "cpu", residual=False)
+    assert op.sum is None
+    with pytest.raises(ValueError, match="sum"):              # a buffer it was made without has a size too
+        op.sum = x[:1]
+    dec = B.Decode(p, "cpu")
+    dec.idx = dec.gate = None
+    assert dec.idx is None

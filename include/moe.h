@@ -440,8 +440,8 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
  * Root-mean-square norm with the residual's addition, per token row:
  *   s[t] = x[t] + residual[t],  rstd[t] = (mean_c s[t][c]^2 + eps)^(-1/2),
  *   y[t][c] = s[t][c] rstd[t] weight[c]
- * in float32; sum and y are rounded to nearest even where they are stored (y
- * from the unrounded s).  For MOE_MXFP8 problems the rows' MXFP8 form can be
+ * with the squares summed in float64; sum and y are rounded to nearest even
+ * where they are stored (y from the unrounded s).  For MOE_MXFP8 problems the rows' MXFP8 form can be
  * written in the same pass: E4M3 codes and E8M0 scales of the stored bf16 y
  * (MXFP8 as above, blocks of 32 along d), which moe_forward_quantized reads
  * ("Section 24: Conclusion", 24.3: a quantiser should emit what the consumer
@@ -540,7 +540,8 @@ int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, con
  *   ws       : device, moe_router_backward_workspace_bytes (host-only query;
  *              may be 0: then ws may be NULL)
  * Tensors are 16-byte aligned.  Sums run in a fixed order.  Errors:
- * MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an unaligned pointer. */
+ * MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an unaligned pointer or
+ * dx == x. */
 int32_t moe_router_backward_workspace_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const void* x, const void* w_router,
                             const void* dx_in, void* dx, float* dw_router, void* ws, size_t ws_bytes, void* stream);

@@ -17,7 +17,7 @@
 // All of it is bound by HBM: every tensor is read or written once.  A row
 // stays in registers between its reduction and its output.  Forward, T = 32768,
 // d = 2048, MXFP8 rows with residual and codes: 94 us, 6.4 TB/s; backward,
-// T = 16384, d = 4096, bf16 with dsum: 101 us, 5.3 TB/s (a 2 GiB copy runs at
+// T = 16384, d = 4096, bf16 with dsum: 98 us, 5.5 TB/s (a 2 GiB copy runs at
 // 4.9 TB/s on the same card).
 #include <algorithm>
 
@@ -200,7 +200,9 @@ struct NormBwdArgs {
 // registers; the workgroup's groups are added in order into one partial row.
 // A workgroup per row once a row has more than two chunks a lane (a wave per
 // row of 4096 bf16 values needs 370 registers: one wave a SIMD, 120 us against
-// 111 at T = 16384); streams that exceed the caches non-temporal (111 -> 101).
+// 111 at T = 16384); streams that exceed the caches non-temporal (111 -> 101);
+// the next row requested before a row is summed (101 -> 98 with half as many
+// workgroups; T = 32768, d = 2048: 106 -> 99; two rows ahead 104).
 template <bool BF, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int NV = BF ? 8 : 4;
@@ -216,17 +218,31 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
         for (int i = 0; i < 8; ++i) dw[g][i] = 0.f;
     }
     const int t0 = (blockIdx.x * NG + grp) * a.rows, t1 = min(a.T, t0 + a.rows);
-    for (int t = t0; t < t1; ++t) {
+    u32x4 sn[CH], yn[CH], en[CH];   // the next row, in flight while this one is summed and stored
+    float rn = 0.f;
+    auto load = [&](int t) {
         const size_t row = (size_t)t * a.chunks;
-        u32x4 sr[CH], yr[CH], er[CH];
 #pragma unroll
         for (int g = 0; g < CH; ++g) {
             const int c = min(lt + TPR * g, a.chunks - 1);
-            sr[g] = stream_load<NT>(a.s + row + c);
-            yr[g] = stream_load<NT>(a.dy + row + c);
-            if (a.dsum) er[g] = stream_load<NT>(a.dsum + row + c);
+            sn[g] = stream_load<NT>(a.s + row + c);
+            yn[g] = stream_load<NT>(a.dy + row + c);
+            if (a.dsum) en[g] = stream_load<NT>(a.dsum + row + c);
         }
-        const float rstd = a.rstd[t];
+        rn = a.rstd[t];
+    };
+    if (t0 < t1) load(t0);
+    for (int t = t0; t < t1; ++t) {
+        const size_t row = (size_t)t * a.chunks;
+        u32x4 sr[CH], yr[CH], er[CH];
+        const float rstd = rn;
+#pragma unroll
+        for (int g = 0; g < CH; ++g) {
+            sr[g] = sn[g];
+            yr[g] = yn[g];
+            er[g] = en[g];
+        }
+        if (t + 1 < t1) load(t + 1);
         float dot = 0.f;
 #pragma unroll
         for (int g = 0; g < CH; ++g) {
@@ -378,7 +394,10 @@ struct NormBwdPlan {
     int blocks;   // partial rows of the weight gradient
 };
 
-constexpr int kNormPartials = 512;   // two workgroups per compute unit
+// Two workgroups per compute unit; one where a row takes a workgroup's threads
+// more than once and the tensors pass the caches (T = 16384, d = 4096, bf16: 98 us
+// against 102; T = 32768, d = 2048: 119 against 99).
+constexpr int kNormPartials = 512;
 
 NormBwdPlan norm_bwd_plan(int T, int chunks) {
     NormBwdPlan p{};
@@ -389,7 +408,8 @@ NormBwdPlan norm_bwd_plan(int T, int chunks) {
         p.tpr = 256;
         p.ch = chunks <= 256 ? 1 : (chunks <= 512 ? 2 : 4);
     }
-    const int groups = kNormPartials * (p.tpr == 64 ? 4 : 1);
+    const bool one = p.tpr == 256 && p.ch > 1 && past_caches((size_t)T * chunks * 16);
+    const int groups = (one ? kNormPartials / 2 : kNormPartials) * (p.tpr == 64 ? 4 : 1);
     p.rows = (T + groups - 1) / groups;
     const int per_block = p.rows * (p.tpr == 64 ? 4 : 1);
     p.blocks = (T + per_block - 1) / per_block;

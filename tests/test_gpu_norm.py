@@ -134,7 +134,7 @@ def test_norm_backward(T, d, act, dsum):
     u, n = np.abs(dy64 * w64), np.abs(s64 * r64[:, None])
     mag = r64[:, None] * (u + n * (u * n).mean(1, keepdims=True)) + (0 if ds_in is None else np.abs(as_f64(ds_in)))
     _close("ds", g["ds"], ds_ref, HALF[act] * np.abs(ds_ref) + 160 * U * mag)
-    # the weight gradient: T <= 5000 rows, at most 10 per thread, then 4 and 512 / 16 partial sums and 16 waves
+    # the weight gradient: T <= 5000 rows, at most 17 per thread, then 4 and 512 / 16 partial sums and 16 waves
     _close("dweight", g["dweight"], dw_ref, 80 * U * (np.abs(dy64) * n).sum(0))
 
 

@@ -370,16 +370,18 @@ __global__ __launch_bounds__(256) void router_dx_resident_kernel(const float* __
 // latency bound it, and a dL block is three times an x block, so with 64
 // experts two waves share the columns and a wave's tile is 128 columns by 32
 // experts (44 us at T = 16384, d = 4096, E = 64; 32 by 64: 50 us).  Two
-// buffers, and the loads of the next PD tiles in flight.
+// buffers, and the loads of the next PD tiles in flight (43 us; with loads
+// behind a test for the range's end, where a tile waits for every later one's,
+// 46; two workgroups joined in one, for half as many partial sums, 46).
 template <bool BF, int NT, int CT>
-__global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict__ dL, const void* __restrict__ x,
+__global__ __launch_bounds__(256, 2) void router_dw_kernel(const float* __restrict__ dL, const void* __restrict__ x,
                                                         float* __restrict__ part, int T, int d, int E, int rows) {
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s* lp;
     constexpr int TA = BF ? 1 : 3;
     constexpr int kTile = 32 * 32 + 32;                 // bytes of a 16-column block, padded
     constexpr int NX = BF ? 1 : 2;                      // 16-byte loads of 8 columns
-    constexpr int PD = BF && NT < 4 ? 4 : 2;            // as many as the registers of two waves a SIMD hold
+    constexpr int PD = BF && NT < 4 ? 4 : 2;            // (four tiles of 64 experts: 47 us)
     constexpr int XI = CT / 64;                         // 8-column items of a thread: 32 tokens x CT / 8 chunks
     constexpr int WE = NT == 4 ? 2 : 1, WC = 4 / WE;    // waves over the experts, over the columns
     constexpr int MT = CT / WC / 16, NW = NT / WE;      // a wave's blocks
@@ -402,26 +404,24 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
     // this thread's columns and expert, clamped (what is past d or E is not stored)
     const uint32_t xc = (uint32_t)min(c0 + 8 * lc, d - 8) / (BF ? 8 : 4);
     const int be = min(e0 + 16 * min(wave, NT - 1) + m, E - 1);
+    // A tile is the 32 rows from tb, or the range's last 32 if they end before tb + 32 (all of them if it is shorter):
+    // every load is unconditional, so that a tile waits for its own loads alone, and stage() clears the other rows.
+    const int nrow = min(32, t1 - t0), last = t1 - nrow;
+    uint32_t xo[XI], bo[8];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xo[i] = (uint32_t)(min(lt + 2048 / CT * i, nrow - 1) * rowc) + xc;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bo[j] = (uint32_t)min(8 * q + j, nrow - 1) * (uint32_t)E + be;
     auto load = [&](int tb, u32x4 (&xr)[XI][NX], float (&br)[8]) {
-        const u32x4* xt = static_cast<const u32x4*>(x) + (size_t)tb * rowc;   // uniform, as are the rows' steps
+        tb = min(tb, last);
+        const u32x4* xt = static_cast<const u32x4*>(x) + (size_t)tb * rowc;   // uniform
         const float* lb = dL + (size_t)tb * E;
-        if (tb + 32 <= t1) {
 #pragma unroll
-            for (int i = 0; i < XI; ++i)
+        for (int i = 0; i < XI; ++i)
 #pragma unroll
-                for (int g = 0; g < NX; ++g)
-                    xr[i][g] = (xt + 2048 / CT * i * rowc)[(uint32_t)(lt * rowc) + xc + g];
+            for (int g = 0; g < NX; ++g) xr[i][g] = xt[xo[i] + g];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) br[j] = (lb + (size_t)j * E)[(uint32_t)(8 * q * E + be)];
-        } else {   // the last tile: rows clamped, and staged as zero
-            const int last = t1 - 1 - tb;
-#pragma unroll
-            for (int i = 0; i < XI; ++i)
-#pragma unroll
-                for (int g = 0; g < NX; ++g) xr[i][g] = xt[min(lt + 2048 / CT * i, last) * rowc + xc + g];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) br[j] = lb[(size_t)min(8 * q + j, last) * E + be];
-        }
+        for (int j = 0; j < 8; ++j) br[j] = lb[bo[j]];
     };
     auto stage = [&](int buf, int tb, u32x4 (&xr)[XI][NX], float (&br)[8]) {
 #pragma unroll
@@ -430,7 +430,8 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
             const int off = (lc >> 1) * kTile + tl * 32 + (lc & 1) * 16;
             if (tb + 32 > t1) {
 #pragma unroll
-                for (int g = 0; g < NX; ++g) xr[i][g] = tb + tl < t1 ? xr[i][g] : (u32x4){0u, 0u, 0u, 0u};
+                for (int g = 0; g < NX; ++g)
+                    xr[i][g] = min(tb, last) + tl >= tb && tl < nrow ? xr[i][g] : (u32x4){0u, 0u, 0u, 0u};
             }
             if constexpr (BF) {
                 *reinterpret_cast<u32x4*>(&s_x[buf][0][off]) = xr[i][0];
@@ -448,7 +449,7 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
             bf16x8 o[3];
             if (tb + 32 > t1) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) br[j] = tb + 8 * q + j < t1 ? br[j] : 0.f;
+                for (int j = 0; j < 8; ++j) br[j] = min(tb, last) + 8 * q + j >= tb && 8 * q + j < nrow ? br[j] : 0.f;
             }
             split3(br, o);
 #pragma unroll
@@ -457,13 +458,12 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
     };
 
 #pragma unroll
-    for (int u = 0; u < PD; ++u)
-        if (t0 + 32 * u < t1) load(t0 + 32 * u, xr[u], br[u]);
+    for (int u = 0; u < PD; ++u) load(t0 + 32 * u, xr[u], br[u]);
     auto tile = [&](int tb, int u) {
         const int buf = u & 1;
         stage(buf, tb, xr[u], br[u]);
         __syncthreads();   // also: every wave has left the buffer that is written next
-        if (tb + 32 * PD < t1) load(tb + 32 * PD, xr[u], br[u]);
+        load(tb + 32 * PD, xr[u], br[u]);
         bf16x8 b[NW][3];
 #pragma unroll
         for (int nt = 0; nt < NW; ++nt)
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(256) void router_dw_kernel(const float* __restrict_
     for (int tb = t0; tb < t1; tb += 32 * PD) {
 #pragma unroll
         for (int u = 0; u < PD; ++u)
-            if (tb + 32 * u < t1) tile(tb + 32 * u, u);
+            tile(tb + 32 * u, u);   // past the range: nothing but zeros
     }
     float* dst = part + (size_t)blockIdx.z * d * E;
 #pragma unroll
@@ -539,7 +539,7 @@ RouterDwPlan router_dw_plan(int act, int T, int d, int E) {
     p.wy = (E + 16 * p.nt - 1) / (16 * p.nt);
     const int want = std::max(1, 512 / (p.wx * p.wy));
     const int ranges = std::max(1, std::min(want, (T + 127) / 128));
-    p.rows = ((T + ranges - 1) / ranges + 31) / 32 * 32;
+    p.rows = ((T + ranges - 1) / ranges + 63) / 64 * 64;
     p.S = (T + p.rows - 1) / p.rows;
     return p;
 }

@@ -40,8 +40,16 @@ __device__ __forceinline__ float group_max(float v) {
     return __uint_as_float(group_reduce<G>(__float_as_uint(v), MaxF32{}));
 }
 
-// The V logits of this lane (experts V r .. V r + V, -inf past E), then their
-// softmax and log-sum-exp over the group.  A row without a finite logit has
+// Value v of lane r of a group: runs of four, so that a load's lanes are side by
+// side (16 values of a lane in a row: T = 8192, E = 1024, 10.8 us forward and 24.8
+// backward; so 10.3 and 18.5).
+template <int G>
+__device__ __forceinline__ int expert_of(int r, int v) {
+    return 4 * G * (v / 4) + 4 * r + v % 4;
+}
+
+// The V logits of this lane (-inf past E), then their softmax and log-sum-exp
+// over the group.  A row without a finite logit has
 // no distribution: p = 0, lse = 0.
 template <int G, int V>
 __device__ __forceinline__ void row_softmax(const float (&l)[V], float (&p)[V], float& lse) {
@@ -63,23 +71,23 @@ __device__ __forceinline__ void row_softmax(const float (&l)[V], float (&p)[V], 
     lse = none ? 0.f : mx + logf(z);
 }
 
-template <int V>
-__device__ __forceinline__ void load_logits(const float* logits, size_t t, int E, int e0, float (&l)[V]) {
+template <int G, int V>
+__device__ __forceinline__ void load_logits(const float* logits, size_t t, int E, int r, float (&l)[V]) {
     const float* row = logits + t * E;
     if ((E & 3) == 0) {   // whole runs of four, 16 bytes aligned
 #pragma unroll
         for (int v = 0; v < V; v += 4) {
-            const f32x4 q = *reinterpret_cast<const f32x4*>(row + min(e0 + v, E - 4));
+            const f32x4 q = *reinterpret_cast<const f32x4*>(row + min(expert_of<G>(r, v), E - 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) l[v + i] = q[i];
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = row[min(e0 + v, E - 1)];
+        for (int v = 0; v < V; ++v) l[v] = row[min(expert_of<G>(r, v), E - 1)];
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (e0 + v >= E) l[v] = -INFINITY;
+        if (expert_of<G>(r, v) >= E) l[v] = -INFINITY;
 }
 
 }  // namespace
@@ -114,7 +122,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(const floa
         for (int u = 0; u < kTok; ++u) {
             const int t = tb + TA * u + grp, tc = min(t, T - 1);
             live[u] = t < t1 && (mask == nullptr || mask[tc] != 0);
-            load_logits<V>(logits, (size_t)tc, E, V * r, l[u]);
+            load_logits<G, V>(logits, (size_t)tc, E, r, l[u]);
         }
 #pragma unroll
         for (int u = 0; u < kTok; ++u) {
@@ -159,7 +167,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(const floa
     }
     if (lane < G) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) s_p[wave][V * r + v] = ps[v];
+        for (int v = 0; v < V; ++v) s_p[wave][expert_of<G>(r, v)] = ps[v];
     }
     if (lane == 0) {
         s_z[wave] = zs;
@@ -324,7 +332,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
     float f[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        f[v] = V * r + v < E ? (float)counts[min(V * r + v, E - 1)] * inv / (float)k : 0.f;
+        f[v] = expert_of<G>(r, v) < E ? (float)counts[min(expert_of<G>(r, v), E - 1)] * inv / (float)k : 0.f;
     const int tb = blockIdx.x * TA * kTok;
     float l[kTok][V];
     bool live[kTok];
@@ -332,7 +340,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
     for (int u = 0; u < kTok; ++u) {
         const int tc = min(tb + TA * u + grp, T - 1);
         live[u] = mask == nullptr || mask[tc] != 0;
-        load_logits<V>(logits, (size_t)tc, E, V * r, l[u]);
+        load_logits<G, V>(logits, (size_t)tc, E, r, l[u]);
     }
 #pragma unroll
     for (int u = 0; u < kTok; ++u) {
@@ -349,12 +357,12 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
         if ((E & 3) == 0) {
 #pragma unroll
             for (int v = 0; v < V; v += 4)
-                if (V * r + v < E)
-                    *reinterpret_cast<f32x4*>(row + V * r + v) = (f32x4){p[v], p[v + 1], p[v + 2], p[v + 3]};
+                if (expert_of<G>(r, v) < E)
+                    *reinterpret_cast<f32x4*>(row + expert_of<G>(r, v)) = (f32x4){p[v], p[v + 1], p[v + 2], p[v + 3]};
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (V * r + v < E) row[V * r + v] = p[v];
+                if (expert_of<G>(r, v) < E) row[expert_of<G>(r, v)] = p[v];
         }
     }
 }
@@ -362,7 +370,8 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
 namespace {
 
 // Lanes per token: the smallest power of two G <= 64 with E / G <= 4
-// (V = 4 logits a lane; at E > 256 all 64 lanes hold up to 16).
+// (V = 4 logits a lane; at E > 256 all 64 lanes hold 8, or up to 16 beyond 512:
+// T = 16384, E = 512, 9.7 us forward and 17 backward with 8, 13.7 and 22 with 16).
 int balance_lanes(int E) {
     int G = 1;
     while (G < 64 && (E + G - 1) / G > 4) G <<= 1;
@@ -418,6 +427,7 @@ hipError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t
         case 32: partial_t<32, 4>(logits, idx, mask, T, E, k, part, cnt, counts, loss, s); break;
         default:
             if (E <= 256) partial_t<64, 4>(logits, idx, mask, T, E, k, part, cnt, counts, loss, s);
+            else if (E <= 512) partial_t<64, 8>(logits, idx, mask, T, E, k, part, cnt, counts, loss, s);
             else partial_t<64, 16>(logits, idx, mask, T, E, k, part, cnt, counts, loss, s);
     }
     const int nblk = balance_blocks(T, E);
@@ -440,6 +450,7 @@ hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const in
         case 32: bwd_t<32, 4>(logits, mask, counts, dloss, T, E, k, dlogits, s); break;
         default:
             if (E <= 256) bwd_t<64, 4>(logits, mask, counts, dloss, T, E, k, dlogits, s);
+            else if (E <= 512) bwd_t<64, 8>(logits, mask, counts, dloss, T, E, k, dlogits, s);
             else bwd_t<64, 16>(logits, mask, counts, dloss, T, E, k, dlogits, s);
     }
     return hipGetLastError();

@@ -68,7 +68,7 @@ def _check_balance(logits, idx, mask, k, dloss=(0.3, 0.05)):
 # the lanes-per-token variants (E 1 .. 1024), token counts of one workgroup and of many
 @pytest.mark.parametrize("T, E, k", [(1, 1, 1), (1, 4, 4), (5, 3, 2), (300, 8, 2), (1000, 12, 3), (777, 20, 4),
                                      (2049, 64, 8), (700, 128, 4), (513, 200, 6), (300, 260, 16), (40, 1024, 16),
-                                     (40000, 8, 2)])
+                                     (40000, 8, 2), (70, 301, 3), (200, 512, 4), (90, 513, 2), (150, 700, 4)])
 @pytest.mark.parametrize("padded", ["no", "some", "all"])
 def test_balance(T, E, k, padded):
     print(f"[balance] T={T} E={E} k={k} padded={padded}", flush=True)

@@ -40,12 +40,13 @@ __device__ __forceinline__ float group_max(float v) {
     return __uint_as_float(group_reduce<G>(__float_as_uint(v), MaxF32{}));
 }
 
-// Value v of lane r of a group: runs of four, so that a load's lanes are side by
-// side (16 values of a lane in a row: T = 8192, E = 1024, 10.8 us forward and 24.8
-// backward; so 10.3 and 18.5).
+// Expert of value v of lane r of a group, so that a load's lanes are side by side:
+// runs of four where rows are 16 bytes aligned (16 values of a lane in a row:
+// T = 8192, E = 1024, 10.8 us forward and 24.8 backward; so 10.3 and 18.5), else
+// one (T = 13725, E = 277: with runs of four 10.5 and 15.8 us, so 10.1 and 13.9).
 template <int G>
-__device__ __forceinline__ int expert_of(int r, int v) {
-    return 4 * G * (v / 4) + 4 * r + v % 4;
+__device__ __forceinline__ int expert_of(int E, int r, int v) {
+    return (E & 3) == 0 ? 4 * G * (v / 4) + 4 * r + v % 4 : G * v + r;
 }
 
 // The V logits of this lane (-inf past E), then their softmax and log-sum-exp
@@ -77,17 +78,17 @@ __device__ __forceinline__ void load_logits(const float* logits, size_t t, int E
     if ((E & 3) == 0) {   // whole runs of four, 16 bytes aligned
 #pragma unroll
         for (int v = 0; v < V; v += 4) {
-            const f32x4 q = *reinterpret_cast<const f32x4*>(row + min(expert_of<G>(r, v), E - 4));
+            const f32x4 q = *reinterpret_cast<const f32x4*>(row + min(expert_of<G>(E, r, v), E - 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) l[v + i] = q[i];
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = row[min(expert_of<G>(r, v), E - 1)];
+        for (int v = 0; v < V; ++v) l[v] = row[min(expert_of<G>(E, r, v), E - 1)];
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (expert_of<G>(r, v) >= E) l[v] = -INFINITY;
+        if (expert_of<G>(E, r, v) >= E) l[v] = -INFINITY;
 }
 
 }  // namespace
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(const floa
     }
     if (lane < G) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) s_p[wave][expert_of<G>(r, v)] = ps[v];
+        for (int v = 0; v < V; ++v) s_p[wave][expert_of<G>(E, r, v)] = ps[v];
     }
     if (lane == 0) {
         s_z[wave] = zs;
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
     float f[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        f[v] = expert_of<G>(r, v) < E ? (float)counts[min(expert_of<G>(r, v), E - 1)] * inv / (float)k : 0.f;
+        f[v] = expert_of<G>(E, r, v) < E ? (float)counts[min(expert_of<G>(E, r, v), E - 1)] * inv / (float)k : 0.f;
     const int tb = blockIdx.x * TA * kTok;
     float l[kTok][V];
     bool live[kTok];
@@ -357,12 +358,12 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const float* logits,
         if ((E & 3) == 0) {
 #pragma unroll
             for (int v = 0; v < V; v += 4)
-                if (expert_of<G>(r, v) < E)
-                    *reinterpret_cast<f32x4*>(row + expert_of<G>(r, v)) = (f32x4){p[v], p[v + 1], p[v + 2], p[v + 3]};
+                if (expert_of<G>(E, r, v) < E)
+                    *reinterpret_cast<f32x4*>(row + expert_of<G>(E, r, v)) = (f32x4){p[v], p[v + 1], p[v + 2], p[v + 3]};
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (expert_of<G>(r, v) < E) row[expert_of<G>(r, v)] = p[v];
+                if (expert_of<G>(E, r, v) < E) row[expert_of<G>(E, r, v)] = p[v];
         }
     }
 }

@@ -6,10 +6,11 @@
 //   y = s rstd w.
 // The squares are summed in float64; s and y are each rounded once, where they
 // are stored, and y is computed from the unrounded s.  For MXFP8 blocks the
-// row's E4M3 codes and E8M0 scales are written in the same pass.  They are the codes of the stored bf16 y (the arithmetic of
-// quantize_mxfp8_kernel), so an MXFP8 forward fed with them is bit for bit the
-// forward fed with y; the extra rounding is half a bf16 step, 2^-8 of a value,
-// against the 2^-4 of the E4M3 rounding that follows.
+// row's E4M3 codes and E8M0 scales are written in the same pass.  They are the
+// codes of the stored bf16 y (the arithmetic of quantize_mxfp8_kernel), so an
+// MXFP8 forward fed with them is bit for bit the forward fed with y; the extra
+// rounding is half a bf16 step, 2^-8 of a value, against the 2^-4 of the E4M3
+// rounding that follows.
 //
 // Backward, with n = s rstd and u = dy w:
 //   ds = rstd (u - n mean(u n)) + dsum,   dw = sum over tokens of dy n.

@@ -510,7 +510,8 @@ int32_t moe_forward_quantized(const moe_problem* p, const void* x, const uint8_t
  * zero for tokens that are not live.  N = 0 gives zeros.  Uses T, n_experts
  * and top_k of the problem.
  *   logits : device float32 [T, E]; -inf excludes an expert from the softmax,
- *            a live row of -inf alone counts as p = 0, lse = 0; rows that are
+ *            a live row of -inf alone counts as p = 0, lse = 0; NaN in a live
+ *            row makes both losses and that row's gradient NaN; rows that are
  *            not live may hold anything
  *   topk_idx : device int32 [T, k]; an index outside [0, E) is not counted
  *   mask   : device uint8 [T], nonzero: the token is live; NULL: all are

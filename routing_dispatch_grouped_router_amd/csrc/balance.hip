@@ -50,26 +50,27 @@ __device__ __forceinline__ int expert_of(int E, int r, int v) {
 }
 
 // The V logits of this lane (-inf past E), then their softmax and log-sum-exp
-// over the group.  A row without a finite logit has
-// no distribution: p = 0, lse = 0.
+// over the group.  A row of -inf alone has no distribution: p = 0, lse = 0.
+// fmaxf passes NaN over, so such a row is told by its sum, which is 0 for it
+// alone: a finite or infinite maximum adds 1 or NaN, and a NaN logit NaN.
 template <int G, int V>
 __device__ __forceinline__ void row_softmax(const float (&l)[V], float (&p)[V], float& lse) {
     float mx = l[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) mx = fmaxf(mx, l[v]);
     mx = group_max<G>(mx);
-    const bool none = mx == -INFINITY;
+    if (mx == -INFINITY) mx = 0.f;
     float z = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        p[v] = none ? 0.f : expf(l[v] - mx);
+        p[v] = expf(l[v] - mx);
         z += p[v];
     }
     z = group_sum<G>(z);
-    const float inv = none ? 0.f : 1.0f / z;
+    const float inv = z == 0.f ? 0.f : 1.0f / z;
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] *= inv;
-    lse = none ? 0.f : mx + logf(z);
+    lse = z == 0.f ? 0.f : mx + logf(z);
 }
 
 template <int G, int V>

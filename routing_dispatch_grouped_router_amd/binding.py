@@ -561,7 +561,8 @@ class NormBackward(_Operator):
 
 class BalanceLoss(_Operator):
     """Preallocated outputs and workspace of moe_balance_loss and its backward:
-    loss [2] (balance, z), counts [E], live [1] (tokens), dlogits [T, E]."""
+    loss [2] (balance, z), counts_live [E + 1] and its parts counts [E] and live [1]
+    (tokens), dlogits [T, E]."""
 
     def __init__(self, p: Problem, device):
         super().__init__(p, device)
@@ -569,8 +570,15 @@ class BalanceLoss(_Operator):
         self._buffer("ws", (_bytes("moe_balance_workspace_bytes", p),), torch.uint8)
         self._buffer("loss", (2,), torch.float32)
         self._buffer("counts_live", (p.n_experts + 1,), torch.int32)
-        self.counts, self.live = self.counts_live[:-1], self.counts_live[-1:]
         self._buffer("dlogits", self._shape, torch.float32)
+
+    @property
+    def counts(self):
+        return self.counts_live[:-1]
+
+    @property
+    def live(self):
+        return self.counts_live[-1:]
 
     def _expect_logits(self, logits, mask):
         _expect(logits, self._shape, torch.float32, "logits")

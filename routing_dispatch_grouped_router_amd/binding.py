@@ -377,6 +377,9 @@ class Forward:
         self.y = torch.empty((T, d), dtype=out_dtype(p.act), device=device)
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
         self.debug = debug_outputs
+        # whether the last call ran on code rows, which stay outside the workspace: what a Backward has to be given
+        # (a replayed graph does not pass here: set it where the graph's forward was the other kind)
+        self.quantized = False
         self.router_stats = (torch.empty((E + 2,), dtype=torch.float32, device=device) if stats else None)
         if debug_outputs:
             self.idx = torch.empty((T, k), dtype=torch.int32, device=device)
@@ -416,6 +419,7 @@ class Forward:
                 *args, ctypes.c_void_p(self.host_counts.data_ptr())))
         else:
             _check("moe_forward", lib().moe_forward(*args))
+        self.quantized = xq is not None
         return self.y
 
 
@@ -476,9 +480,12 @@ class Backward:
     def __call__(self, fwd: "Forward", dy, packed, packed_bwd, x=None, w_router=None, stream=None,
                  dlogits_aux=None, xq=None):
         """dlogits_aux [T, E]: a gradient for the logits to be added (BalanceLoss.backward's);
-        xq: the codes the forward was given, if it was given any."""
+        xq: the codes the forward was given, required if it was given any."""
         p = self.p
         dt = storage_dtype(p.act)
+        if (xq is not None) != fwd.quantized:
+            raise ValueError("xq: expected the codes that the forward ran on" if fwd.quantized else
+                             "xq: not expected, the forward did not run on codes")
         if dlogits_aux is not None:
             _expect(dlogits_aux, (p.T, p.n_experts), torch.float32, "dlogits_aux")
         if xq is not None:

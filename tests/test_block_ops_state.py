@@ -1,5 +1,5 @@
-"""What the operators' objects keep from call to call: checked on the host (no
-GPU needed)."""
+"""What the operators' objects keep from call to call, and calls that do not go
+together: checked on the host (no GPU needed)."""
 import pytest
 import torch
 
@@ -8,6 +8,22 @@ from routing_dispatch_grouped_router_amd import binding as B
 
 def _p(T=64, d=256, E=8, k=2, H=256, act="mxfp8", **kw):
     return B.problem(T, d, E, k, H, act, **kw)
+
+
+@pytest.fixture
+def accepting(monkeypatch):
+    """A library that takes every call, for host tensors."""
+    real, calls = B.lib(), []
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return getattr(real, name)
+            return lambda *a: calls.append(name) or 0
+    monkeypatch.setattr(B, "lib", lambda: Lib())
+    monkeypatch.setattr(B, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(B, "_stream", lambda *a, **k: 0)
+    return calls
 
 
 def test_counts_follow_the_buffer_put_in_place(monkeypatch):
@@ -21,3 +37,45 @@ def test_counts_follow_the_buffer_put_in_place(monkeypatch):
     for name in ("counts", "live"):                           # parts of counts_live, not buffers
         with pytest.raises(AttributeError):
             setattr(op, name, other[:1])
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_backward_takes_the_codes_its_forward_took(accepting, given):
+    p = _p(logits_given=given)
+    fwd, bwd = B.Forward(p, "cpu"), B.Backward(p, "cpu", aux=True)
+    x, w = torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(256, 8, dtype=torch.bfloat16)
+    q, qs = torch.zeros(64, 256, dtype=torch.uint8), torch.zeros(64, 8, dtype=torch.uint8)
+    kw = dict(logits=torch.zeros(64, 8)) if given else dict(w_router=w)
+    rows = dict(x=x, w_router=None if given else w)
+
+    def back(**more):
+        return bwd(fwd, x, None, w, **rows, **more)
+    fwd(x, packed=w, xq=q, xq_scale=qs, **kw)
+    del accepting[:]
+    with pytest.raises(ValueError, match="xq"):
+        back()
+    with pytest.raises(ValueError, match="xq"):
+        back(dlogits_aux=torch.zeros(64, 8))
+    assert not accepting
+    back(xq=q)
+    back(xq=q.clone())                                        # the same codes kept elsewhere
+    fwd(x, packed=w, **kw)
+    del accepting[:]
+    with pytest.raises(ValueError, match="xq"):
+        back(xq=q)
+    assert not accepting
+    back()
+    back(dlogits_aux=torch.zeros(64, 8))
+    # a call that was refused leaves what the workspace holds
+    fwd(x, packed=w, xq=q, xq_scale=qs, **kw)
+    with pytest.raises(ValueError):
+        fwd(x[:3], packed=w, **kw)
+    back(xq=q)
+
+
+def test_backward_of_a_forward_that_has_not_run(accepting):
+    p = _p()
+    fwd, bwd = B.Forward(p, "cpu"), B.Backward(p, "cpu")
+    x, w = torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(256, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="xq"):
+        bwd(fwd, x, None, w, x=x, w_router=w, xq=torch.zeros(64, 256, dtype=torch.uint8))

@@ -555,8 +555,9 @@ int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const vo
  * arguments as moe_backward; ws_bytes >= moe_backward_aux_workspace_bytes.
  * With both NULL it is moe_backward.  Errors: as moe_backward; MOE_ERR_DTYPE /
  * MOE_ERR_SHAPE for xq on a problem moe_forward_quantized does not take;
- * MOE_ERR_ARG for an unaligned xq (16), for dlogits_aux == dlogits, and with
- * dlogits_aux for dlogits, w_router, x, dx or ws not 16-byte aligned. */
+ * MOE_ERR_ARG for an unaligned xq (16), for dlogits_aux == dlogits, with
+ * dlogits_aux for dlogits, w_router, x, dx or ws not 16-byte aligned, and with
+ * dlogits_aux or xq for dx == x where the router is learned. */
 int32_t moe_backward_aux_workspace_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, const void* w_router,
                          const void* packed_w, const void* packed_bwd, const int32_t* topk_idx,

@@ -796,6 +796,8 @@ static int32_t backward_impl(const moe_problem* p, const void* dy, const void* x
     const Layout L = layout(*p);
     const BwdLayout BL = bwd_layout(*p);
     if (fwd_ws_bytes < L.total || ws_bytes < (aux ? bwd_aux_bytes(*p) : BL.total)) return MOE_ERR_WORKSPACE;
+    // x is read for dw_router after dx is written (moe_backward_aux; moe_backward's checks are as they were)
+    if (!given && (aux || xq) && dx == x) return MOE_ERR_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int T = p->T, E = p->n_experts, k = p->top_k, d = p->d_model, H = p->d_hidden;
     const int R = T * k, act = bwd_act(p->act_dtype);

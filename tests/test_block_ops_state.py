@@ -1,9 +1,14 @@
 """What the operators' objects keep from call to call, and calls that do not go
 together: checked on the host (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
 from routing_dispatch_grouped_router_amd import binding as B
+
+F = ctypes.c_void_p(0x1000)
+G = ctypes.c_void_p(0x3000)
 
 
 def _p(T=64, d=256, E=8, k=2, H=256, act="mxfp8", **kw):
@@ -79,3 +84,12 @@ def test_backward_of_a_forward_that_has_not_run(accepting):
     x, w = torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(256, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="xq"):
         bwd(fwd, x, None, w, x=x, w_router=w, xq=torch.zeros(64, 256, dtype=torch.uint8))
+
+
+def test_dx_over_x_is_refused_where_x_is_read_after_it():
+    """dw_router is made from x after dx is written, in the dense gradient and in the sparse one."""
+    for act, aux, xq in (("mxfp8", G, None), ("mxfp8", G, F), ("mxfp8", None, F), ("bf16", G, None), ("f32", G, None)):
+        p, n = _p(act=act), ctypes.c_size_t()
+        assert B.lib().moe_backward_aux_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == 0
+        assert B.lib().moe_backward_aux(ctypes.byref(p), F, F, F, F, F, None, None, None, None, F, B.workspace_bytes(p), F,
+                                        F, F, F, F, F, F, n.value, None, aux, xq) == -7

@@ -532,7 +532,8 @@ int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, con
 /* Gradients of the router's product logits = x W_r from dense logit gradients:
  *   dx[t] = dx_in[t] + sum_e dlogits[t][e] W_r[:, e],   dw_router = x^T dlogits
  * accumulated in float32 (float32 operands enter the matrix cores as three
- * bfloat16 terms each), dx rounded once.
+ * bfloat16 terms each), dx rounded once.  Infinite and NaN operands give what
+ * the sums of products give.
  *   dlogits  : device float32 [T, E]
  *   x        : device [T, d] activation type (bf16 for MOE_MXFP8)
  *   w_router : device [d, E], same type

@@ -10,6 +10,10 @@
 // remainder of the ones before), and the products of terms i, j with
 // i + j <= 4 are summed in the float32 accumulators: what is left out is below
 // 2^-24 of the product.  dL is always split, x and W_r only for float32 blocks.
+// The terms of an infinity, and of a value that rounds past bfloat16's largest,
+// are not its sum but NaN, and a zero remainder times an infinity is NaN too, so
+// a sum that comes out NaN is taken again in float32 from the operands: it is
+// then what the products give, +-inf or NaN.
 #include <algorithm>
 
 #include "moe_device.h"
@@ -93,6 +97,45 @@ __device__ __forceinline__ void load_terms_full(const void* p, uint32_t i, bf16x
         const f32x4 hi = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i + 4);
         const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         split3(v, o);
+    }
+}
+
+// Value i of an operand in memory.
+template <bool BF>
+__device__ __forceinline__ float value_at(const void* p, size_t i) {
+    return BF ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// Whether one of N sums is NaN.
+template <int N>
+__device__ __forceinline__ bool any_nan(const float (&v)[N]) {
+    bool n = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n |= v[i] != v[i];
+    return n;
+}
+
+// Whether a lane of the wave has a NaN sum.
+template <int M, int N>
+__device__ __forceinline__ bool wave_nan(const f32x4 (&acc)[M][N]) {
+    bool n = false;
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) n |= any_nan({acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]});
+    return __any(n);
+}
+
+// v[j] = sum_e dL[t][e] W_r[c + j][e] in float32, for the rows whose sums of terms are NaN.
+template <bool BF>
+__device__ __forceinline__ void row_product(const float* dL, const void* w, int t, int c, int E, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll 1
+    for (int e = 0; e < E; ++e) {
+        const float g = dL[(size_t)t * E + e];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(g, value_at<BF>(w, (size_t)(c + j) * E + e), v[j]);
     }
 }
 
@@ -206,39 +249,61 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
         return BF ? __uint_as_float((j & 1) ? (c[0][j / 2] & 0xFFFF0000u) : (c[0][j / 2] << 16))
                   : __uint_as_float(c[NC == 1 ? 0 : j / 4][j % 4]);
     };
+    // row t: `b` or the gathered rows, plus the product's sums
+    auto finish = [&](int t, const u32x4 (&b)[NC], const float (&sum)[8]) {
+        float v[8];
+        if (pos) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            for (int s = 0; s < k; ++s) {
+                const size_t r = (size_t)pos[(size_t)t * k + s];
+                u32x4 c[NC];
+#pragma unroll
+                for (int g = 0; g < NC; ++g) c[g] = src[r * row_chunks + cb + g];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += value(c, j);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = src ? value(b, j) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += sum[j];
+#pragma unroll
+        for (int g = 0; g < NC; ++g) {
+            u32x4 o;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                o[h] = BF ? pack_bf16x2(v[2 * h], v[2 * h + 1]) : __float_as_uint(v[4 * g + h]);
+            dst[t * row_chunks + cb + g] = o;
+        }
+    };
+    auto row_sums = [&](int mt, int i, float (&sum)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = acc[mt][j][i];
+    };
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = wt + 16 * mt + 4 * q + i;
-            if (t >= T) continue;
-            float v[8];
-            if (pos) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.f;
-                for (int s = 0; s < k; ++s) {
-                    const size_t r = (size_t)pos[(size_t)t * k + s];
-                    u32x4 c[NC];
-#pragma unroll
-                    for (int g = 0; g < NC; ++g) c[g] = src[r * row_chunks + cb + g];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += value(c, j);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = src ? value(base[mt][i], j) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += acc[mt][j][i];
-#pragma unroll
-            for (int g = 0; g < NC; ++g) {
-                u32x4 o;
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    o[h] = BF ? pack_bf16x2(v[2 * h], v[2 * h + 1]) : __float_as_uint(v[4 * g + h]);
-                dst[t * row_chunks + cb + g] = o;
-            }
+            float sum[8];
+            row_sums(mt, i, sum);
+            if (t < T) finish(t, base[mt][i], sum);
         }
+    if (wave_nan(acc)) {   // those rows again (what was added is in base: dx may be add)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = wt + 16 * mt + 4 * q + i;
+                float sum[8];
+                row_sums(mt, i, sum);
+                if (t >= T || !any_nan(sum)) continue;
+                row_product<BF>(dL, w, t, wc + 8 * m, E, sum);
+                finish(t, base[mt][i], sum);
+            }
+    }
 }
 
 // The same for bfloat16 blocks of at most 32 NS experts (two 32's fit the LDS
@@ -248,9 +313,9 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
 // d = 4096, E = 64, 4.2 TB/s, of it 2 us by passing the caches (the kernel
 // above: 73); 15 us at T = 8192, d = 2048, E = 8 (17).
 template <int NS, bool NT>
-__global__ __launch_bounds__(256) void router_dx_resident_kernel(const float* __restrict__ dL,
-                                                                 const uint16_t* __restrict__ w, const u32x4* add,
-                                                                 u32x4* dx, int T, int d, int E, int rows) {
+__global__ __launch_bounds__(256, 2) void router_dx_resident_kernel(const float* __restrict__ dL,
+                                                                    const uint16_t* __restrict__ w, const u32x4* add,
+                                                                    u32x4* dx, int T, int d, int E, int rows) {
     __shared__ u32x4 s_w[NS][16][64];
     __shared__ u32x4 s_a[2][NS][4][3][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
@@ -342,20 +407,42 @@ __global__ __launch_bounds__(256) void router_dx_resident_kernel(const float* __
             }
         }
         u32x4* dt = dx + (size_t)t0 * row_chunks;
+        auto finish = [&](int t, const u32x4& b, const float (&sum)[8]) {   // row t0 + t: the row added, plus the sums
+            u32x4 o;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t c = add ? b[h] : 0u;
+                o[h] = pack_bf16x2(__uint_as_float(c << 16) + sum[2 * h],
+                                   __uint_as_float(c & 0xFFFF0000u) + sum[2 * h + 1]);
+            }
+            stream_store<NT>(dt + ((uint32_t)t * row_chunks + cb), o);
+        };
+        auto row_sums = [&](int mt, int i, float (&sum)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = acc[mt][j][i];
+        };
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = 32 * (wave & 1) + 16 * mt + 4 * q + i;
-                u32x4 o;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint32_t c = add ? base[mt][i][h] : 0u;
-                    o[h] = pack_bf16x2(__uint_as_float(c << 16) + acc[mt][2 * h][i],
-                                       __uint_as_float(c & 0xFFFF0000u) + acc[mt][2 * h + 1][i]);
-                }
-                if (in_cols && t0 + t < te) stream_store<NT>(dt + ((uint32_t)t * row_chunks + cb), o);
+                float sum[8];
+                row_sums(mt, i, sum);
+                if (in_cols && t0 + t < te) finish(t, base[mt][i], sum);
             }
+        if (wave_nan(acc)) {   // those rows again (what was added is in base: dx may be add)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 32 * (wave & 1) + 16 * mt + 4 * q + i;
+                    float sum[8];
+                    row_sums(mt, i, sum);
+                    if (!in_cols || t0 + t >= te || !any_nan(sum)) continue;
+                    row_product<true>(dL, w, t0 + t, wc + 8 * m, E, sum);
+                    finish(t, base[mt][i], sum);
+                }
+        }
         if (add && t0 + 64 < te) load_base(t0 + 64);
     }
 }
@@ -492,6 +579,7 @@ __global__ __launch_bounds__(256, 2) void router_dw_kernel(const float* __restri
             tile(tb + 32 * u, u);   // past the range: nothing but zeros
     }
     float* dst = part + (size_t)blockIdx.z * d * E;
+    uint32_t again = 0;   // blocks with a NaN sum
 #pragma unroll
     for (int nt = 0; nt < NW; ++nt) {
         const int e = e0 + 16 * (wn + nt) + m;
@@ -500,9 +588,24 @@ __global__ __launch_bounds__(256, 2) void router_dw_kernel(const float* __restri
         for (int mt = 0; mt < MT; ++mt) {
             const int c = c0 + 16 * (wm + mt) + 4 * q;
             if (c >= d) continue;   // d % 64 == 0: whole blocks
+            const float sum[4] = {acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]};
+            if (any_nan(sum)) again |= 1u << (nt * MT + mt);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[(size_t)(c + i) * E + e] = acc[mt][nt][i];
+            for (int i = 0; i < 4; ++i) dst[(size_t)(c + i) * E + e] = sum[i];
         }
+    }
+    while (again != 0) {   // in float32 from the operands, over what was written
+        const int b = __ffs((int)again) - 1, e = e0 + 16 * (wn + b / MT) + m, c = c0 + 16 * (wm + b % MT) + 4 * q;
+        again &= again - 1;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t) {
+            const float g = dL[(size_t)t * E + e];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = fmaf(g, value_at<BF>(x, (size_t)t * d + c + i), sum[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[(size_t)(c + i) * E + e] = sum[i];
     }
 }
 

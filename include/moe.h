@@ -570,10 +570,11 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
 /* ---------------------------------------------------------------- a few tokens (serving)
  *
  * The block for up to MOE_DECODE_MAX_TOKENS tokens with 4-bit expert weights:
- * x, h, y bfloat16, weights MXFP4 (OCP Microscaling v1.0: E2M1 codes, one E8M0
- * scale per 32 consecutive elements along the contraction axis, shared
- * exponent floor(log2(amax)) - 2 clamped to [-127, 127], elements rounded to
- * nearest even and saturated to +-6).  act_dtype MOE_BF16 or MOE_MXFP8 (no
+ * x and y bfloat16, h two bfloat16 terms (2^-16 of it left out), weights MXFP4
+ * (OCP Microscaling v1.0: E2M1 codes, one E8M0 scale per 32 consecutive elements
+ * along the contraction axis, 255 for NaN; packed with the shared exponent
+ * floor(log2(amax)) - 2 clamped to [-127, 127], elements rounded to nearest even
+ * and saturated to +-6).  act_dtype MOE_BF16 or MOE_MXFP8 (no
  * difference here), d_model and d_hidden multiples of 128, no
  * MOE_IDENTITY_EXPERTS.
  *

@@ -450,14 +450,21 @@ __device__ __forceinline__ void wide_product(GroupRows& s_g, WideStage<NB, NT>& 
 }
 
 // silu(a) b of four hidden units as two bfloat16 terms, at dst and H further.
+// The first term ends at bfloat16's largest value: rounded on to infinity, the
+// remainder would be -inf and the products' sum NaN.  (An infinite or NaN value
+// is its second term.)  The remainder is that of the rounded product in every
+// kernel: without the pragma one of them may fuse the two operations.
 __device__ __forceinline__ void store_h(const f32x4& a, const f32x4& b, uint16_t* dst, int H) {
-    float o[4], lo[4];
+#pragma clang fp contract(off)
+    constexpr float kMax = 0x1.fep127f;
+    float hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        o[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-        lo[i] = o[i] - bf16_round(o[i]);
+        const float o = a[i] / (1.0f + expf(-a[i])) * b[i];
+        hi[i] = bf16_round(fminf(fmaxf(o, -kMax), kMax));
+        lo[i] = o - hi[i];
     }
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
     *reinterpret_cast<uint2*>(dst + H) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
 }
 

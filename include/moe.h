@@ -574,9 +574,9 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  * (OCP Microscaling v1.0: E2M1 codes, one E8M0 scale per 32 consecutive elements
  * along the contraction axis, 255 for NaN; packed with the shared exponent
  * floor(log2(amax)) - 2 clamped to [-127, 127], elements rounded to nearest even
- * and saturated to +-6).  act_dtype MOE_BF16 or MOE_MXFP8 (no
- * difference here), d_model and d_hidden multiples of 128, no
- * MOE_IDENTITY_EXPERTS.
+ * and saturated to +-6, a block with a NaN given the scale 255).  act_dtype
+ * MOE_BF16 or MOE_MXFP8 (no difference here), d_model and d_hidden multiples of
+ * 128, no MOE_IDENTITY_EXPERTS.
  *
  * moe_pack_weights_decode quantises w_gate, w_up [E, d, H], w_down [E, H, d]
  * (device bfloat16) into packed, moe_decode_weight_bytes() bytes:

@@ -668,8 +668,9 @@ __device__ __forceinline__ uint32_t e2m1_encode(float v) {
 
 // MXFP4 of bfloat16 weights [E][K][N] (the x . W convention): destination row
 // n holds column n, a thread one scale block of 32 k of it.  Shared exponent
-// floor(log2(amax)) - 2, clamped to [-127, 127].  GU: the destination rows are
-// W1's, gathered from gate (a) and up (b).  Setup, not timed.
+// floor(log2(amax)) - 2, clamped to [-127, 127]; 255, the scale that is NaN, for a
+// block with a NaN.  GU: the destination rows are W1's, gathered from gate (a)
+// and up (b).  Setup, not timed.
 template <bool GU>
 __global__ __launch_bounds__(256) void pack_mxfp4_kernel(const uint16_t* __restrict__ a,
                                                          const uint16_t* __restrict__ b, int E, int K, int N,
@@ -682,10 +683,12 @@ __global__ __launch_bounds__(256) void pack_mxfp4_kernel(const uint16_t* __restr
     const int col = GU ? 32 * (n >> 6) + (n & 31) : n;
     const uint16_t* src = (GU && ((n >> 5) & 1) ? b : a) + ((size_t)e * K + 32 * kb) * N + col;
     float v[32], amax = 0.f;
+    bool nan = false;   // fmaxf passes it over, and E2M1 has no code for it
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         v[i] = bf16_to_f32(src[(size_t)i * N]);
         amax = fmaxf(amax, fabsf(v[i]));
+        nan |= v[i] != v[i];
     }
     const int ef = (int)((__float_as_uint(amax) >> 23) & 0xFF);
     const int se = ef == 0 ? -127 : max(ef - 127 - 2, -127);
@@ -696,7 +699,7 @@ __global__ __launch_bounds__(256) void pack_mxfp4_kernel(const uint16_t* __restr
     for (int i = 0; i < 32; ++i) o[i / 8] |= e2m1_encode(v[i] * s0 * s1) << (4 * (i % 8));
     const size_t row = (size_t)e * rows + n;
     *reinterpret_cast<u32x4*>(codes + row * (K / 2) + 16 * kb) = o;
-    scales[row * (K / 32) + kb] = (uint8_t)(se + 127);
+    scales[row * (K / 32) + kb] = nan ? (uint8_t)255 : (uint8_t)(se + 127);
 }
 
 hipError_t launch_pack_mxfp4(const void* w_gate, const void* w_up, const void* w_down, uint8_t* w1, uint8_t* w2,

@@ -1,6 +1,6 @@
 """The 4-bit experts at the ends of their format and of the hidden units' range
-(marked gpu): scale bytes near 0 (2^-127) and 255 (NaN in OCP MX v1.0), hidden
-units past bfloat16's largest value.
+(marked gpu): scale bytes near 0 (2^-127) and 255 (NaN in OCP MX v1.0), NaN
+weights when they are packed, hidden units past bfloat16's largest value.
 
 The finite values are held to the float64 oracle with its bound (float32 sums,
 h to 2^-16 of it, y rounded once: 2^-8)."""
@@ -90,6 +90,28 @@ def test_scale_byte_255_is_nan(T, d, E, k, H):
         got = _run(p, x, idx, gate, packed)
         assert np.isnan(got[uses]).all() and np.array_equal(got[~uses], good[~uses])
         s1[e, row, 0] = keep
+
+
+def test_packing_keeps_nan():
+    E, d, H = 3, 256, 128
+    rng = np.random.default_rng(5)
+    w = [torch.from_numpy((0.05 * rng.standard_normal(s)).astype(np.float32)).to(torch.bfloat16)
+         for s in ((E, d, H), (E, d, H), (E, H, d))]
+    p = B.problem(1, d, E, 1, H, "bf16")
+    good = B.pack_weights_decode(p, *(t.to(DEV) for t in w)).cpu().numpy()
+    w[0][1, 40, 3] = float("nan")                             # gate unit 3 of expert 1, its second block
+    w[2][2, 100, 7] = float("nan")
+    packed = B.pack_weights_decode(p, *(t.to(DEV) for t in w)).cpu().numpy()
+    n = np.cumsum([E * H * d, E * d * H // 2, E * H * d // 16, E * d * H // 32])
+    want = good[n[1]:].copy()
+    want[:n[2] - n[1]].reshape(E, 2 * H, d // 32)[1, 3, 1] = 255
+    want[n[2] - n[1]:].reshape(E, d, H // 32)[2, 7, 3] = 255
+    assert np.array_equal(packed[n[1]:], want)
+    x = torch.ones((1, d), dtype=torch.bfloat16)
+    gate = np.ones((1, 1), np.float32)
+    for e, cols in ((0, []), (1, list(range(d))), (2, [7])):
+        y = _run(p, x, np.full((1, 1), e, np.int32), gate, packed)[0]
+        assert np.flatnonzero(np.isnan(y)).tolist() == cols
 
 
 @pytest.mark.parametrize("T, d, E, k, H", SHAPES)

@@ -440,8 +440,9 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
  * Root-mean-square norm with the residual's addition, per token row:
  *   s[t] = x[t] + residual[t],  rstd[t] = (mean_c s[t][c]^2 + eps)^(-1/2),
  *   y[t][c] = s[t][c] rstd[t] weight[c]
- * with the squares summed in float64; sum and y are rounded to nearest even
- * where they are stored (y from the unrounded s), for rows of any finite sums
+ * with s the float32 sum and its squares summed in float64; sum and y are
+ * rounded to nearest even where they are stored (y from the float32 s), for
+ * rows of any finite sums
  * (rstd itself is infinite past float32's range).  For MOE_MXFP8 problems the
  * rows' MXFP8 form can be written in the same pass: E4M3 codes and E8M0 scales
  * of the stored bf16 y (MXFP8 as above, blocks of 32 along d), which

@@ -4,8 +4,8 @@
 // Forward, per token row of d values:
 //   s = x + r (r the residual; none: s = x),  rstd = (mean(s^2) + eps)^(-1/2),
 //   y = s rstd w.
-// The squares are summed in float64; s and y are each rounded once, where they
-// are stored, and y is computed from the unrounded s.  For MXFP8 blocks the
+// s is the float32 sum; its squares are summed in float64; s and y are each
+// rounded once, where they are stored, and y is computed from the float32 s.  For MXFP8 blocks the
 // row's E4M3 codes and E8M0 scales are written in the same pass.  They are the
 // codes of the stored bf16 y (the arithmetic of quantize_mxfp8_kernel), so an
 // MXFP8 forward fed with them is bit for bit the forward fed with y; the extra
@@ -133,9 +133,11 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     }
     // The row times a power of two, sc, that brings its mean square to [1, 4): the root, its reciprocal and s w stay in
     // float32's range for every row of finite values.  rstd of it as two floats (one step of Newton's method from the
-    // rounded root), and y from them and the two halves of s w: y is the float32 nearest to the exact value, so that a
-    // code or a scale at a rounding border is the exact value's too.  Four more operations a value than s rstd w,
-    // hidden behind the loads (32768 x 2048 with codes: 94 us with one of them, sc, and 93 without).
+    // rounded root), and y from them and the two halves of s w: y is the float32 nearest to the exact value for the
+    // float32 s, so that a code or a scale at a rounding border is that value's too.  (What the addition of a residual
+    // rounds away, up to 2^-24 of s, is left out: with it carried into y the rows of one chunk a thread took longer,
+    // 32768 x 2048 with codes 99.7 us instead of 92.5, 8000 x 1024 13.3 instead of 10.5.)  Four more operations a value
+    // than s rstd w, hidden behind the loads (32768 x 2048: 94 us with one of them, sc, and 93 without).
     const double ms = row_sum<TPR>(ss, red) * a.inv_d + a.eps;
     const int ex = (int)((unsigned long long)__double_as_longlong(ms) >> 52) - 1023;   // ms >= 0
     const int k = min(max(ex >> 1, -126), 126);

@@ -1,6 +1,6 @@
 """The norm over the whole range of its types (marked gpu): every value held to
 the float64 oracle, NaN or an unwritten output among them counted as wrong;
-rows whose squares leave float32's range.
+rows whose squares leave float32's range; y to the last float32 bit.
 
 A stored value is off by half a step of its type (bf16 2^-8, float32 2^-24 of
 it); 160 half-steps (u = 2^-24) bound what float32 arithmetic adds."""
@@ -133,3 +133,45 @@ def test_a_row_of_zeros_without_eps_has_no_norm():
     op = _norm(x, w, None, "bf16", 0.0)
     assert op.y[[0, 2]].isnan().all() and op.rstd[[0, 2]].isinf().all()
     assert torch.equal(op.y[1].cpu(), torch.ones(256, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp8", "f32"])
+@pytest.mark.parametrize("T, d", [(8000, 512), (2000, 2048), (500, 8192), (250, 16512)])
+def test_y_is_the_float32_nearest_for_the_float32_sum(T, d, act):
+    """Residuals so far below x that the sum is rounded: y is the float32 next to the exact value for the rounded sum,
+    rounded to its type; where 2^-40 of it decide, either."""
+    print(f"[norm nearest] T={T} d={d} {act}", flush=True)
+    rng = np.random.default_rng(T)
+    x = _rand(rng, (T, d), act)
+    r = (_rand(rng, (T, d), "f32") * torch.from_numpy(2.0 ** rng.integers(-20, -10, (T, d))).float()).to(x.dtype)
+    w = _rand(rng, (d,), act)
+    op = _norm(x, w, r, act, 1e-6)
+    s = as_f64(x.float() + r.float())
+    assert (s != as_f64(x) + as_f64(r)).mean() > 0.1
+    _, _, y = Q.rmsnorm(s, None, as_f64(w), 1e-6)
+    lo, hi = (torch.from_numpy((y * f).astype(np.float32)).to(x.dtype) for f in (1 - 2.0 ** -40, 1 + 2.0 ** -40))
+    got = op.y.cpu()
+    wrong = (got != lo) & (got != hi)
+    assert not wrong.any(), f"{int(wrong.sum())} of {y.size} values"
+    if act == "mxfp8":
+        codes, scales = MX.quantize(as_f64(op.y))
+        assert np.array_equal(op.q.cpu().numpy(), codes) and np.array_equal(op.q_scale.cpu().numpy(), scales)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_an_infinity_leaves_its_row_zeros_and_a_nan(residual, act):
+    rng = np.random.default_rng(6)
+    x, w = _rand(rng, (5, 1024), act), torch.ones(1024).to(B.storage_dtype(act))
+    r = _rand(rng, (5, 1024), act) if residual else None
+    good = _norm(x, w, r, act, 1e-6).y.clone()
+    x[2, 7] = -float("inf")
+    if residual:
+        r[3, 9] = float("inf")
+        x[4, 0], r[4, 0] = float("inf"), -float("inf")
+    op = _norm(x, w, r, act, 1e-6)
+    y = op.y.clone()
+    assert torch.equal(y[:2], good[:2]) and op.rstd[2] == 0 and y[2, 7].isnan() and int((y[2] != 0).sum()) == 1
+    if residual:
+        assert op.rstd[3] == 0 and y[3, 9].isnan() and int((y[3] != 0).sum()) == 1 and op.sum[3, 9].isinf()
+        assert y[4].isnan().all()

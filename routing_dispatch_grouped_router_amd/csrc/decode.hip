@@ -25,7 +25,7 @@
 // does not depend on the tokens beside it.
 //
 // The weights' bytes bound it.  d = 4096, E = 64, k = 8, H = 1536: one token 20 us
-// (80 MB, 4.0 TB/s), 64 tokens 145 us (643 MB, 4.4 TB/s); T = 7, d = 2048, E = 128,
+// (80 MB, 3.9 TB/s), 64 tokens 144 us (643 MB, 4.5 TB/s); T = 7, d = 2048, E = 128,
 // k = 4, H = 1024: 20 us (63 MB, 3.1 TB/s; two launches of 2.5 us and more whatever
 // they read).  A 2 GiB copy runs at 4.9 TB/s on the same card.
 #include "moe_device.h"
@@ -713,9 +713,9 @@ hipError_t launch_pack_mxfp4(const void* w_gate, const void* w_up, const void* w
 
 // Workgroups from which the kernels with their waves side by side are taken:
 // two on every compute unit.  T = 64, d = 4096, E = 64, k = 8, H = 1536 (1536
-// and 2048 of them): 152 us against 169 with the waves on the quarters of K,
-// T = 256: 273 and 359; T = 16, E = 8, k = 2, H = 1536 (192 and 256): 18.4 + 10.5
-// us the two products against 13.2 + 9.3.
+// and 2048 of them): the kernels together 151 us against 171 with the waves on
+// the quarters of K, T = 256: 302 and 372; T = 16, E = 8, k = 2, H = 1536 (192
+// and 256): 18.4 + 10.5 us the two products against 13.2 + 9.3.
 // With no more rows than experts a group mostly holds one row, few activations
 // to share: the up projection then keeps its waves on the quarters (T = 12,
 // d = 4096, E = 64, k = 4, H = 1536: 46 us against 55); the down projection, with

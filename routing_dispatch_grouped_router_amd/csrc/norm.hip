@@ -17,7 +17,7 @@
 //
 // All of it is bound by HBM: every tensor is read or written once.  A row
 // stays in registers between its reduction and its output.  Forward, T = 32768,
-// d = 2048, MXFP8 rows with residual and codes: 94 us, 6.4 TB/s; backward,
+// d = 2048, MXFP8 rows with residual and codes: 94 us, 6.5 TB/s; backward,
 // T = 16384, d = 4096, bf16 with dsum: 98 us, 5.5 TB/s (a 2 GiB copy runs at
 // 4.9 TB/s on the same card).
 #include <algorithm>
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
     // float32 s, so that a code or a scale at a rounding border is that value's too.  (What the addition of a residual
     // rounds away, up to 2^-24 of s, is left out: with it carried into y the rows of one chunk a thread took longer,
     // 32768 x 2048 with codes 99.7 us instead of 92.5, 8000 x 1024 13.3 instead of 10.5.)  Four more operations a value
-    // than s rstd w, hidden behind the loads (32768 x 2048: 94 us with one of them, sc, and 93 without).
+    // than s rstd w, hidden behind the loads (32768 x 2048 with codes: 94 us, without the one for sc 93).
     const double ms = row_sum<TPR>(ss, red) * a.inv_d + a.eps;
     const int ex = (int)((unsigned long long)__double_as_longlong(ms) >> 52) - 1023;   // ms >= 0
     const int k = min(max(ex >> 1, -126), 126);

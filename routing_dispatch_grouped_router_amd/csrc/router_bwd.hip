@@ -146,10 +146,10 @@ __device__ __forceinline__ void row_product(const float* dL, const void* w, int 
 // block j is column 8 n + j, so that a lane's eight blocks hold 8 consecutive
 // columns of a token and sixteen lanes 128: add is read and dx written in whole
 // lines (a lane layout with a row per lane cost the memory pipe an access per
-// lane, 126 us at T = 16384, d = 4096, E = 64; 73 us so).  Both operands pass through LDS
-// in fragment order, 32 experts at a time, loaded in whole 64- and 128-byte
-// pieces and split once for the workgroup; two buffers, the next experts' loads
-// in flight during a step's products.  `add`: row t of add (pos NULL; requested
+// lane: 1.7 times as long at T = 16384, d = 4096, E = 64, where this takes 64 us).
+// Both operands pass through LDS in fragment order, 32 experts at a time, loaded
+// in whole 64- and 128-byte pieces and split once for the workgroup; two buffers,
+// the next experts' loads in flight during a step's products.  `add`: row t of add (pos NULL; requested
 // before the products), or the sum of its rows pos[t][0 .. k), or nothing (NULL).
 template <bool BF>
 __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict__ dL, const void* __restrict__ w,
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
     // thread: experts 8 (tid % 4) .. of token tid / 4 and of columns tid / 4 + 64 i
     const int lr = tid >> 2, lq = tid & 3;
     // (uniform bases and 32-bit lane offsets, and a path without the test for the last expert: address and select
-    // instructions held this kernel up, 79 us with a 64-bit offset and a test a load at the size above, 73 us so)
+    // instructions held this kernel up: 8 % longer with a 64-bit offset and a test a load)
     const float* dl0 = dL + (size_t)t0 * E;
     const char* w0 = static_cast<const char*>(w) + (size_t)c0 * E * (BF ? 2 : 4);
     const uint32_t dlo = (uint32_t)min(lr, T - 1 - t0) * (uint32_t)E + 8 * lq;
@@ -309,9 +309,10 @@ __global__ __launch_bounds__(256) void router_dx_kernel(const float* __restrict_
 // The same for bfloat16 blocks of at most 32 NS experts (two 32's fit the LDS
 // of two workgroups) and rows added one for one: a workgroup keeps its 256
 // columns of W_r in LDS and walks `rows` tokens, 64 at a time, the next tokens'
-// dL and rows of add in flight during a tile's products.  64 us at T = 16384,
-// d = 4096, E = 64, 4.2 TB/s, of it 2 us by passing the caches (the kernel
-// above: 73); 15 us at T = 8192, d = 2048, E = 8 (17).
+// dL and rows of add in flight during a tile's products.  55 us at T = 16384,
+// d = 4096, E = 64, 4.9 TB/s (the kernel above: 64; through the caches 58, and
+// dW_r, which reads x from them, 43 instead of 34); 17 us at T = 8192, d = 2048,
+// E = 8 (19).
 template <int NS, bool NT>
 __global__ __launch_bounds__(256, 2) void router_dx_resident_kernel(const float* __restrict__ dL,
                                                                     const uint16_t* __restrict__ w, const u32x4* add,
@@ -456,10 +457,11 @@ __global__ __launch_bounds__(256, 2) void router_dx_resident_kernel(const float*
 // experts 16 nt .. + 16, and shared through LDS.  LDS reads and the tiles'
 // latency bound it, and a dL block is three times an x block, so with 64
 // experts two waves share the columns and a wave's tile is 128 columns by 32
-// experts (44 us at T = 16384, d = 4096, E = 64; 32 by 64: 50 us).  Two
-// buffers, and the loads of the next PD tiles in flight (43 us; with loads
-// behind a test for the range's end, where a tile waits for every later one's,
-// 46; two workgroups joined in one, for half as many partial sums, 46).
+// experts (32 us at T = 16384, d = 4096, E = 64, and 7 for the ranges' sum; the
+// two 14 % longer with 32 by 64).  Two buffers, and the loads of the next PD
+// tiles in flight (7 % longer with loads behind a test for the range's end,
+// where a tile waits for every later one's; as much with two workgroups joined
+// in one, for half as many partial sums).
 template <bool BF, int NT, int CT>
 __global__ __launch_bounds__(256, 2) void router_dw_kernel(const float* __restrict__ dL, const void* __restrict__ x,
                                                         float* __restrict__ part, int T, int d, int E, int rows) {
@@ -468,7 +470,7 @@ __global__ __launch_bounds__(256, 2) void router_dw_kernel(const float* __restri
     constexpr int TA = BF ? 1 : 3;
     constexpr int kTile = 32 * 32 + 32;                 // bytes of a 16-column block, padded
     constexpr int NX = BF ? 1 : 2;                      // 16-byte loads of 8 columns
-    constexpr int PD = BF && NT < 4 ? 4 : 2;            // (four tiles of 64 experts: 47 us)
+    constexpr int PD = BF && NT < 4 ? 4 : 2;            // (four tiles of 64 experts: 9 % longer)
     constexpr int XI = CT / 64;                         // 8-column items of a thread: 32 tokens x CT / 8 chunks
     constexpr int WE = NT == 4 ? 2 : 1, WC = 4 / WE;    // waves over the experts, over the columns
     constexpr int MT = CT / WC / 16, NW = NT / WE;      // a wave's blocks
@@ -661,7 +663,7 @@ void launch_router_dw_t(const float* dL, const void* x, float* dst, const Router
 
 // Workgroups of the resident kernel: two rounds of the two that a compute unit
 // holds (T = 16384, d = 4096, E = 64 and T = 8192, d = 2048, E = 8: 512 of them
-// 67 and 19 us, 1024 66 and 16, 2048 68 and 16).
+// 56 and 21 us, 1024 55 and 17, 2048 59 and 17).
 constexpr int kDxGroups = 1024;
 
 hipError_t launch_router_dx(int act, const float* dL, const void* w_router, const void* add, const int32_t* pos, int k,

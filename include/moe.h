@@ -445,8 +445,8 @@ int32_t moe_backward(const moe_problem* p, const void* dy, const void* x, const 
  * rows of any finite sums
  * (rstd itself is infinite past float32's range).  For MOE_MXFP8 problems the
  * rows' MXFP8 form can be written in the same pass: E4M3 codes and E8M0 scales
- * of the stored bf16 y (MXFP8 as above, blocks of 32 along d), which
- * moe_forward_quantized reads
+ * of the stored bf16 y (MXFP8 as above, blocks of 32 along d; NaN saturated, as
+ * moe_forward's own quantiser does), which moe_forward_quantized reads
  * ("Section 24: Conclusion", 24.3: a quantiser should emit what the consumer
  * reads without conversion; Evidence 6 counted separate quantise kernels as
  * overhead).  Uses T, d_model and act_dtype of the problem.

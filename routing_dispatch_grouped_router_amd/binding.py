@@ -510,12 +510,13 @@ class Backward:
 
 class Norm(_Operator):
     """Preallocated outputs of moe_norm: y [T, d], rstd [T], with a residual its
-    sum [T, d], for MXFP8 problems the rows' codes q [T, d] and scales q_scale
-    [T, d/32] (uint8) unless quantized is False."""
+    sum [T, d] (put None in its place where nothing reads it), for MXFP8 problems
+    the rows' codes q [T, d] and scales q_scale [T, d/32] (uint8) unless quantized
+    is False."""
 
     def __init__(self, p: Problem, device, eps: float = 1e-6, residual: bool = True, quantized: bool | None = None):
         super().__init__(p, device)
-        self.eps = float(eps)
+        self.eps, self.residual = float(eps), bool(residual)
         (T, d), dt = self._shape, self._dt = _rows(p)
         if quantized is None:
             quantized = p.act == "mxfp8"
@@ -530,8 +531,10 @@ class Norm(_Operator):
         shape, dt = self._shape, self._dt
         _expect(x, shape, dt, "x")
         _expect(weight, shape[1:], dt, "weight")
-        if (residual is None) != (self.sum is None):
-            raise ValueError("residual: " + ("expected" if residual is None else "not expected"))
+        if residual is None and self.sum is not None:
+            raise ValueError("residual: expected")
+        if residual is not None and self.sum is None and not self.residual:
+            raise ValueError("residual: not expected")
         if residual is not None:
             _expect(residual, shape, dt, "residual")
         _check("moe_norm", lib().moe_norm(

@@ -44,6 +44,27 @@ def test_counts_follow_the_buffer_put_in_place(monkeypatch):
             setattr(op, name, other[:1])
 
 
+def test_norm_of_a_sum_that_is_not_kept(accepting, monkeypatch):
+    """sum is optional: nothing reads that of the last norm."""
+    monkeypatch.setattr(B, "_inputs", lambda device, *t: [None if v is None else v.data_ptr() for v in t])
+    x, w = torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(256, dtype=torch.bfloat16)
+    op = B.Norm(_p(act="bf16"), "cpu")
+    op.sum = None
+    op(x, w, residual=x)
+    op(x, w)                                                  # as before
+    assert accepting == ["moe_norm"] * 2
+    op = B.Norm(_p(act="bf16"), "cpu")
+    with pytest.raises(ValueError, match="residual: expected"):
+        op(x, w)
+    op = B.Norm(_p(act="bf16"), "cpu", residual=False)
+    with pytest.raises(ValueError, match="residual: not expected"):
+        op(x, w, residual=x)
+    op._index = x.get_device()
+    monkeypatch.setattr(B, "_ptr", lambda t: t.data_ptr())
+    op.sum = x.clone()
+    op(x, w, residual=x)
+
+
 @pytest.mark.parametrize("given", [False, True])
 def test_backward_takes_the_codes_its_forward_took(accepting, given):
     p = _p(logits_given=given)

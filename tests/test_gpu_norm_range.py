@@ -175,3 +175,13 @@ def test_an_infinity_leaves_its_row_zeros_and_a_nan(residual, act):
     if residual:
         assert op.rstd[3] == 0 and y[3, 9].isnan() and int((y[3] != 0).sum()) == 1 and op.sum[3, 9].isinf()
         assert y[4].isnan().all()
+
+
+@pytest.mark.parametrize("T, d", [(130, 576), (21, 2048), (3, 16512), (4200, 4096)])
+def test_a_sum_that_is_not_kept(T, d):
+    rng = np.random.default_rng(4)
+    x, r, w = (_rand(rng, sh, "bf16").to(DEV) for sh in ((T, d), (T, d), (d,)))
+    op = B.Norm(B.problem(T, d, 1, 1, 128, "bf16"), DEV)
+    y, rstd = op(x, w, residual=r).clone(), op.rstd.clone()
+    op.sum = None
+    assert torch.equal(op(x, w, residual=r), y) and torch.equal(op.rstd, rstd)

@@ -486,6 +486,36 @@ int32_t moe_norm_backward_workspace_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_norm_backward(const moe_problem* p, const void* dy, const void* dsum, const void* s, const void* weight,
                           const float* rstd, void* ds, float* dweight, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- layer norm in front of the block
+ *
+ * Layer norm with the residual's addition, for models that subtract a row's mean:
+ *   s[t] = x[t] + residual[t],  mean[t] = mean_c s[t][c],
+ *   rstd[t] = (mean_c (s[t][c] - mean[t])^2 + eps)^(-1/2),
+ *   y[t][c] = (s[t][c] - mean[t]) rstd[t] weight[c] + bias[c]
+ * with s the float32 sum, both means and y taken in float64 and rounded to
+ * nearest even where they are stored.  A row of one value everywhere gives the
+ * bias (eps > 0; with eps 0 it is NaN).  MXFP8 codes of the stored y, layouts,
+ * optional arguments and buffers that may be the same are moe_norm's.
+ *   weight   : device [d], activation type
+ *   bias     : device [d], activation type, or NULL: none
+ *   mean     : device float32 [T] out, or NULL (moe_layer_norm_backward reads it)
+ * Errors: as moe_norm, with bias and mean among the pointers. */
+int32_t moe_layer_norm(const moe_problem* p, const void* x, const void* residual, const void* weight, const void* bias,
+                       float eps, void* sum, void* y, uint8_t* yq, uint8_t* yq_scale, float* mean, float* rstd,
+                       void* stream);
+
+/* Gradients of moe_layer_norm: with n = (s - mean) rstd and u = dy weight,
+ *   ds[t] = rstd (u - mean_c(u) - n mean_c(u n)) + dsum[t],
+ *   dweight = sum_t dy n,  dbias = sum_t dy.
+ *   mean, rstd     : device float32 [T] of the forward
+ *   dweight, dbias : device float32 [d] out; dbias may be NULL
+ * Other arguments, in-place use, order of the sums and errors as
+ * moe_norm_backward; ws: moe_layer_norm_backward_workspace_bytes. */
+int32_t moe_layer_norm_backward_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_layer_norm_backward(const moe_problem* p, const void* dy, const void* dsum, const void* s,
+                                const void* weight, const float* mean, const float* rstd, void* ds, float* dweight,
+                                float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 /* moe_forward of a MOE_MXFP8 block (d_model >= 256) whose token rows are
  * already quantised: xq [T, d] codes and xq_scale [T, d/32] as moe_norm
  * writes them (xq 16-byte, xq_scale 4-byte aligned).  No quantise pass runs;

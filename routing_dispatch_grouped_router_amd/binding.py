@@ -28,6 +28,7 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_packe
            "moe_set_gemm_grid_cap", "moe_backward_workspace_bytes", "moe_backward_weight_bytes",
            "moe_pack_weights_backward", "moe_backward", "moe_set_test_flags", "moe_route_noalloc",
            "moe_fused_status", "moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward",
+           "moe_layer_norm", "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
            "moe_forward_quantized", "moe_balance_workspace_bytes", "moe_balance_loss",
            "moe_balance_loss_backward", "moe_router_backward_workspace_bytes", "moe_router_backward",
            "moe_backward_aux_workspace_bytes", "moe_backward_aux", "moe_decode_weight_bytes",
@@ -94,11 +95,13 @@ def lib():
         L.moe_pack_weights_backward.argtypes = [PP, _P, _P, _P, _P, _P]
         L.moe_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P,
                                    _P, _SZ, _P]
-        for name in ("norm_backward_workspace", "balance_workspace", "router_backward_workspace",
+        for name in ("norm_backward_workspace", "layer_norm_backward_workspace", "balance_workspace", "router_backward_workspace",
                      "backward_aux_workspace", "decode_weight", "decode_workspace"):
             getattr(L, f"moe_{name}_bytes").argtypes = [PP, ctypes.POINTER(_SZ)]
         L.moe_norm.argtypes = [PP, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P]
         L.moe_norm_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_layer_norm.argtypes = [PP, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P]
+        L.moe_layer_norm_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_forward_quantized.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_balance_loss.argtypes = [PP, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_balance_loss_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P]
@@ -567,6 +570,73 @@ class NormBackward(_Operator):
             self._p, *_inputs(self._index, dy, dsum, s, weight, rstd), _own(self.ds),
             _own(self.dweight), _own(self.ws), self.ws.numel(), _stream(stream, self._index)))
         return dict(ds=self.ds, dweight=self.dweight)
+
+
+class LayerNorm(_Operator):
+    """Preallocated outputs of moe_layer_norm: y [T, d], mean and rstd [T], with a
+    residual its sum [T, d] (put None in its place where nothing reads it), for
+    MXFP8 problems the rows' codes q [T, d] and scales q_scale [T, d/32] (uint8)
+    unless quantized is False."""
+
+    def __init__(self, p: Problem, device, eps: float = 1e-5, residual: bool = True, quantized: bool | None = None):
+        super().__init__(p, device)
+        self.eps, self.residual = float(eps), bool(residual)
+        (T, d), dt = self._shape, self._dt = _rows(p)
+        if quantized is None:
+            quantized = p.act == "mxfp8"
+        self._buffer("y", (T, d), dt)
+        self._buffer("sum", (T, d), dt, residual)
+        self._buffer("mean", (T,), torch.float32)
+        self._buffer("rstd", (T,), torch.float32)
+        self._buffer("q", (T, d), torch.uint8, quantized)
+        self._buffer("q_scale", (T, d // 32), torch.uint8, quantized)
+
+    def __call__(self, x, weight, bias=None, residual=None, stream=None):
+        """y = layer norm of x + residual, times weight, plus bias; returns y."""
+        shape, dt = self._shape, self._dt
+        _expect(x, shape, dt, "x")
+        _expect(weight, shape[1:], dt, "weight")
+        if bias is not None:
+            _expect(bias, shape[1:], dt, "bias")
+        if residual is None and self.sum is not None:
+            raise ValueError("residual: expected")
+        if residual is not None:
+            if self.sum is None and not self.residual:
+                raise ValueError("residual: not expected")
+            _expect(residual, shape, dt, "residual")
+        _check("moe_layer_norm", lib().moe_layer_norm(
+            self._p, *_inputs(self._index, x, residual, weight, bias), self.eps, _own(self.sum), _own(self.y),
+            _own(self.q), _own(self.q_scale), _own(self.mean), _own(self.rstd), _stream(stream, self._index)))
+        return self.y
+
+
+class LayerNormBackward(_Operator):
+    """Preallocated gradients and workspace of moe_layer_norm_backward; put None in
+    dbias's place for a norm without a bias."""
+
+    def __init__(self, p: Problem, device):
+        super().__init__(p, device)
+        self._shape, self._dt = _rows(p)
+        self._buffer("ws", (_bytes("moe_layer_norm_backward_workspace_bytes", p),), torch.uint8)
+        self._buffer("ds", self._shape, self._dt)
+        self._buffer("dweight", (p.d_model,), torch.float32)
+        self._buffer("dbias", (p.d_model,), torch.float32)
+
+    def __call__(self, dy, s, weight, mean, rstd, dsum=None, stream=None) -> dict:
+        """dy: the gradient of y; s, mean, rstd: the forward's (s is x without a residual); dsum:
+        the gradient of that sum from elsewhere.  dict(ds, dweight, dbias)."""
+        shape, dt = self._shape, self._dt
+        _expect(dy, shape, dt, "dy")
+        _expect(s, shape, dt, "s")
+        _expect(weight, shape[1:], dt, "weight")
+        _expect(mean, shape[:1], torch.float32, "mean")
+        _expect(rstd, shape[:1], torch.float32, "rstd")
+        if dsum is not None:
+            _expect(dsum, shape, dt, "dsum")
+        _check("moe_layer_norm_backward", lib().moe_layer_norm_backward(
+            self._p, *_inputs(self._index, dy, dsum, s, weight, mean, rstd), _own(self.ds), _own(self.dweight),
+            _own(self.dbias), _own(self.ws), self.ws.numel(), _stream(stream, self._index)))
+        return dict(ds=self.ds, dweight=self.dweight, dbias=self.dbias)
 
 
 class BalanceLoss(_Operator):

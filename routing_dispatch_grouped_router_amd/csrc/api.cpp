@@ -980,6 +980,46 @@ int32_t moe_norm_backward(const moe_problem* p, const void* dy, const void* dsum
                                     p->T, p->d_model, static_cast<hipStream_t>(stream)));
 }
 
+// ----------------------------------------------------------------------------- layer norm
+
+int32_t moe_layer_norm(const moe_problem* p, const void* x, const void* residual, const void* weight, const void* bias,
+                       float eps, void* sum, void* y, uint8_t* yq, uint8_t* yq_scale, float* mean, float* rstd,
+                       void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (yq && p->act_dtype != MOE_MXFP8) return MOE_ERR_DTYPE;
+    if (!x || !weight || (!y && !yq) || (yq && !yq_scale)) return MOE_ERR_NULL;
+    if (!std::isfinite(eps) || eps < 0.f || off_by(x, 16) || off_by(residual, 16) || off_by(weight, 16) ||
+        off_by(bias, 16) || off_by(sum, 16) || off_by(y, 16) || off_by(yq, 8) || (yq && off_by(yq_scale, 4)) ||
+        off_by(mean, 4) || off_by(rstd, 4) || (y && y == sum))
+        return MOE_ERR_ARG;
+    return launched(launch_layer_norm(p->act_dtype, x, residual, weight, bias, eps, sum, y, yq, yq_scale, mean, rstd,
+                                      p->T, p->d_model, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_layer_norm_backward_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = align256(layer_norm_bwd_part_bytes(p->act_dtype, p->T, p->d_model));
+    return MOE_OK;
+}
+
+int32_t moe_layer_norm_backward(const moe_problem* p, const void* dy, const void* dsum, const void* s,
+                                const void* weight, const float* mean, const float* rstd, void* ds, float* dweight,
+                                float* dbias, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (!dy || !s || !weight || !mean || !rstd || !ds || !dweight || !ws) return MOE_ERR_NULL;
+    if (off_by(dy, 16) || off_by(dsum, 16) || off_by(s, 16) || off_by(weight, 16) || off_by(mean, 4) ||
+        off_by(rstd, 4) || off_by(ds, 16) || off_by(dweight, 16) || off_by(dbias, 16) || off_by(ws, 16) || ds == s)
+        return MOE_ERR_ARG;
+    if (ws_bytes < align256(layer_norm_bwd_part_bytes(p->act_dtype, p->T, p->d_model))) return MOE_ERR_WORKSPACE;
+    return launched(launch_layer_norm_bwd(p->act_dtype, dy, dsum, s, weight, mean, rstd, ds, dweight, dbias,
+                                          static_cast<float*>(ws), p->T, p->d_model,
+                                          static_cast<hipStream_t>(stream)));
+}
+
 // ----------------------------------------------------------------------------- router losses
 
 int32_t moe_balance_workspace_bytes(const moe_problem* p, size_t* bytes) {

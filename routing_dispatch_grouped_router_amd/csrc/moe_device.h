@@ -132,4 +132,63 @@ __device__ __forceinline__ void stream_store(u32x4* p, const u32x4& v) {
     else *p = v;
 }
 
+// The values of 16 bytes of a row: 8 bfloat16 (BF) or 4 float32.
+template <bool BF>
+__device__ __forceinline__ void unpack16(const u32x4& w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            v[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ u32x4 pack16(const float (&v)[8]) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = BF ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
+    return w;
+}
+
+// Sum over the TPR threads of a row, the same on each (fixed order: butterfly
+// in the wave, then the waves in order).
+template <int TPR, typename V>
+__device__ __forceinline__ V row_sum(V v, V* red) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < TPR / 64; ++w) v += red[w];
+    }
+    return v;
+}
+
+// MXFP8 of a bfloat16 row's 16-byte chunk c: its codes to q[c], and one dword of
+// four scales per 128 columns to qs[c / 16].  Called by the 16 lanes that hold
+// such a slice together (4 lanes one block of 32).
+__device__ __forceinline__ void store_mxfp8_chunk(const u32x4& row, int c, uint2* q, uint32_t* qs) {
+    float f[8];
+    unpack16<true>(row, f);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    amax = fmaxf(amax, __shfl_xor(amax, 1));
+    amax = fmaxf(amax, __shfl_xor(amax, 2));
+    const int se = mx_shared_exp(amax);
+    const float inv = mx_inv_scale(se);
+    q[c] = make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                      e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+    uint32_t sw = (uint32_t)(se + 127) << (8 * ((c >> 2) & 3));
+    sw |= __shfl_xor(sw, 4);
+    sw |= __shfl_xor(sw, 8);
+    if ((c & 15) == 0) qs[c >> 4] = sw;
+}
+
 }  // namespace moe

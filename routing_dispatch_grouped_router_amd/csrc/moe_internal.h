@@ -247,6 +247,18 @@ size_t norm_bwd_part_bytes(int act, int T, int d);
 hipError_t launch_norm_bwd(int act, const void* dy, const void* dsum, const void* s_in, const void* weight,
                            const float* rstd, void* ds, float* dweight, float* part, int T, int d, hipStream_t s);
 
+// ---------------------------------------------------------------- layer norm (layer_norm.hip)
+
+// Per row: s = x + residual, y = (s - mean) rstd weight + bias.  residual, bias, sum, y, q, mean and rstd
+// may be NULL; q as in launch_norm.
+hipError_t launch_layer_norm(int act, const void* x, const void* residual, const void* weight, const void* bias,
+                             float eps, void* sum, void* y, void* q, uint8_t* q_scale, float* mean, float* rstd, int T,
+                             int d, hipStream_t s);
+size_t layer_norm_bwd_part_bytes(int act, int T, int d);
+hipError_t launch_layer_norm_bwd(int act, const void* dy, const void* dsum, const void* s_in, const void* weight,
+                                 const float* mean, const float* rstd, void* ds, float* dweight, float* dbias,
+                                 float* part, int T, int d, hipStream_t s);
+
 // ---------------------------------------------------------------- balance loss (balance.hip)
 
 // Scratch of the forward: part holds this many float, cnt as many int32.

@@ -29,43 +29,6 @@ namespace moe {
 
 namespace {
 
-template <bool BF>
-__device__ __forceinline__ void unpack16(const u32x4& w, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (BF) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        } else {
-            v[i] = __uint_as_float(w[i]);
-        }
-    }
-}
-
-template <bool BF>
-__device__ __forceinline__ u32x4 pack16(const float (&v)[8]) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = BF ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
-    return w;
-}
-
-// Sum over the TPR threads of a row, the same on each (fixed order: butterfly
-// in the wave, then the waves in order).
-template <int TPR, typename V>
-__device__ __forceinline__ V row_sum(V v, V* red) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-    if constexpr (TPR > 64) {
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = red[0];
-#pragma unroll
-        for (int w = 1; w < TPR / 64; ++w) v += red[w];
-    }
-    return v;
-}
-
 struct NormArgs {
     const u32x4* x;
     const u32x4* r;      // NULL: no residual
@@ -161,23 +124,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         const u32x4 yp = pack16<BF>(o);
         if (a.y) stream_store<NT>(a.y + row + c, yp);
         if constexpr (BF) {
-            if (a.q) {   // d % 128 == 0: 16 lanes hold one 128-wide slice, 4 lanes one block of 32
-                float f[8];
-                unpack16<true>(yp, f);
-                float amax = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-                amax = fmaxf(amax, __shfl_xor(amax, 1));
-                amax = fmaxf(amax, __shfl_xor(amax, 2));
-                const int se = mx_shared_exp(amax);
-                const float inv = mx_inv_scale(se);
-                a.q[row + c] = make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                                          e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-                uint32_t sw = (uint32_t)(se + 127) << (8 * ((c >> 2) & 3));
-                sw |= __shfl_xor(sw, 4);
-                sw |= __shfl_xor(sw, 8);
-                if ((c & 15) == 0) a.qs[(size_t)t * (a.chunks / 16) + (c >> 4)] = sw;
-            }
+            if (a.q) store_mxfp8_chunk(yp, c, a.q + row, a.qs + (size_t)t * (a.chunks / 16));
         }
     };
 #pragma unroll

@@ -492,7 +492,7 @@ int32_t moe_norm_backward(const moe_problem* p, const void* dy, const void* dsum
  *   s[t] = x[t] + residual[t],  mean[t] = mean_c s[t][c],
  *   rstd[t] = (mean_c (s[t][c] - mean[t])^2 + eps)^(-1/2),
  *   y[t][c] = (s[t][c] - mean[t]) rstd[t] weight[c] + bias[c]
- * with s the float32 sum, both means and y taken in float64 and rounded to
+ * with s the float32 sum, the means and y taken in float64 from it and rounded to
  * nearest even where they are stored.  A row of one value everywhere gives the
  * bias (eps > 0; with eps 0 it is NaN).  MXFP8 codes of the stored y, layouts,
  * optional arguments and buffers that may be the same are moe_norm's.

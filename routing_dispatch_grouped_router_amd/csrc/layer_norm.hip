@@ -18,7 +18,8 @@
 //
 // All of it is bound by HBM: every tensor is read or written once.  Forward,
 // T = 32768, d = 2048, MXFP8 rows with residual and codes: 99.6 us, 6.1 TB/s;
-// T = 16384, d = 4096, bf16 with residual: 88 us.
+// T = 16384, d = 4096, bf16 with residual: 88 us; its backward with dsum 98 us,
+// 5.5 TB/s (a 2 GiB copy runs at 4.9 TB/s on the same card).
 // Slower forwards: mean and squares in one pass about a value of the row, with s
 // exact in float64 and rows walked with the next in flight (fewer waves for more
 // float64 conversions: 107-122 us); y in float32 and values near a bf16 border
@@ -419,18 +420,133 @@ __global__ __launch_bounds__(1024) void layer_norm_reduce_kernel(const float* __
     }
 }
 
+// Small batches: every gradient in one launch.  Workgroups [0, row_blocks) take
+// a row per wave; the others 8 chunks of columns each over all rows, 128 rows at
+// a time (8 lanes a row, so that they read whole 128-byte pieces), eight loads
+// of a lane in flight, and add the row lanes in a fixed order.  s and dy are
+// read twice, from the caches.  `first`: the workgroup that blockIdx.x 0 is.
+template <bool BF>
+__global__ __launch_bounds__(1024) void layer_norm_bwd_small_kernel(LayerNormBwdArgs a, int row_blocks, int first,
+                                                                    float* __restrict__ dw, float* __restrict__ db) {
+    constexpr int NV = BF ? 8 : 4;
+    constexpr int CH = 2;
+    __shared__ float red[2][16][8 * NV];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x + first;
+    if (b < row_blocks) {
+        const int t = b * 16 + wave;
+        if (t >= a.T) return;
+        const size_t row = (size_t)t * a.chunks;
+        const float mean = a.mean[t], rstd = a.rstd[t];
+        float sv[CH][8], yv[CH][8], wv[CH][8], ev[CH][8];
+#pragma unroll
+        for (int g = 0; g < CH; ++g) {
+            const int c = min(lane + 64 * g, a.chunks - 1);
+            unpack16<BF>(a.s[row + c], sv[g]);
+            unpack16<BF>(a.dy[row + c], yv[g]);
+            unpack16<BF>(a.w[c], wv[g]);
+            if (a.dsum) unpack16<BF>(a.dsum[row + c], ev[g]);
+        }
+        float su = 0.f, sun = 0.f;
+#pragma unroll
+        for (int g = 0; g < CH; ++g) {
+            if (lane + 64 * g >= a.chunks) continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float u = yv[g][i] * wv[g][i];
+                su += u;
+                sun = fmaf(u, (sv[g][i] - mean) * rstd, sun);
+            }
+        }
+        const float2 m = row_sum2<64>(su, sun, nullptr);
+        const float mu = m.x * a.inv_d, mun = m.y * a.inv_d;
+#pragma unroll
+        for (int g = 0; g < CH; ++g) {
+            if (lane + 64 * g >= a.chunks) continue;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float n = (sv[g][i] - mean) * rstd;
+                o[i] = rstd * (fmaf(yv[g][i], wv[g][i], -mu) - n * mun);
+                if (a.dsum) o[i] += ev[g][i];
+            }
+            a.ds[row + lane + 64 * g] = pack16<BF>(o);
+        }
+        return;
+    }
+    const int c = 8 * (b - row_blocks) + (lane & 7);   // chunks % 8 == 0
+    float w[NV], u[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w[i] = u[i] = 0.f;
+    constexpr int kB = 8;
+    for (int r = threadIdx.x >> 3; r < a.T; r += 128 * kB) {
+        u32x4 sr[kB], yr[kB];
+        float mean[kB], rstd[kB];
+#pragma unroll
+        for (int j = 0; j < kB; ++j) {
+            const int t = min(r + 128 * j, a.T - 1);
+            sr[j] = a.s[(size_t)t * a.chunks + c];
+            yr[j] = a.dy[(size_t)t * a.chunks + c];
+            mean[j] = a.mean[t];
+            rstd[j] = a.rstd[t];
+        }
+#pragma unroll
+        for (int j = 0; j < kB; ++j) {
+            if (r + 128 * j >= a.T) continue;
+            float sv[8], yv[8];
+            unpack16<BF>(sr[j], sv);
+            unpack16<BF>(yr[j], yv);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                w[i] = fmaf(yv[i], (sv[i] - mean[j]) * rstd[j], w[i]);
+                u[i] += yv[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int m = 8; m <= 32; m <<= 1) {
+            w[i] += __shfl_xor(w[i], m);
+            u[i] += __shfl_xor(u[i], m);
+        }
+        if (lane < 8) {
+            red[0][wave][NV * lane + i] = w[i];
+            red[1][wave][NV * lane + i] = u[i];
+        }
+    }
+    __syncthreads();
+    const int k = threadIdx.x / (8 * NV), col = threadIdx.x % (8 * NV);
+    if (k < 2) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += red[k][i][col];
+        float* out = k ? db : dw;
+        if (out) out[8 * NV * (b - row_blocks) + col] = v;
+    }
+}
+
 // How a backward of T rows of `chunks` 16-byte chunks runs.
 struct LayerNormBwdPlan {
+    bool small;   // one launch; the rest describes the other kernels
     int tpr;      // threads per row: 64, 256, or 0 for the kernels of long rows
     int ch;       // chunks per thread
     int rows;     // rows per group
     int blocks;   // partial rows
 };
 
-constexpr int kPartials = 512;   // two workgroups per compute unit
+// Two workgroups per compute unit; one where a row takes a workgroup's threads
+// more than once (T = 16384, d = 4096, bf16 with dsum: 98 us against 106;
+// T = 2048: 18.3 against 19.9; T = 32768, d = 2048, once: 118 against 100).
+constexpr int kPartials = 512;
+
+// Rows of up to two chunks a lane that take one launch (a second costs 3 us:
+// T = 777, d = 192, float32: 7.1 us against 9.6 through the binding, T = 1000,
+// d = 1024, bf16: 7.6 against 9.8; T = 2000, d = 1024: 13.1 against 12.2).
+constexpr int kSmallRows = 1024;
 
 LayerNormBwdPlan layer_norm_bwd_plan(int T, int chunks) {
     LayerNormBwdPlan p{};
+    p.small = chunks <= 128 && T <= kSmallRows;
     if (chunks <= 64 * 2) {
         p.tpr = 64;
         p.ch = chunks <= 64 ? 1 : 2;
@@ -438,7 +554,7 @@ LayerNormBwdPlan layer_norm_bwd_plan(int T, int chunks) {
         p.tpr = 256;
         p.ch = chunks <= 256 ? 1 : (chunks <= 512 ? 2 : 4);
     }
-    const int groups = kPartials * (p.tpr == 64 ? 4 : 1);
+    const int groups = p.tpr == 64 ? kPartials * 4 : (p.ch > 1 ? kPartials / 2 : kPartials);
     p.rows = (T + groups - 1) / groups;
     const int per_block = p.rows * (p.tpr == 64 ? 4 : 1);
     p.blocks = (T + per_block - 1) / per_block;
@@ -513,6 +629,20 @@ hipError_t launch_layer_norm_bwd(int act, const void* dy, const void* dsum, cons
     const LayerNormBwdArgs a{static_cast<const u32x4*>(dy), static_cast<const u32x4*>(dsum),
                              static_cast<const u32x4*>(s_in), static_cast<const u32x4*>(weight), mean, rstd,
                              static_cast<u32x4*>(ds), part, T, chunks, p.rows, 1.0f / (float)d};
+    if (p.small) {
+        const int rows = (T + 15) / 16, cols = chunks / 8;
+        auto go = [&](int first, int n) {
+            if (bf) hipLaunchKernelGGL((layer_norm_bwd_small_kernel<true>), dim3(n), dim3(1024), 0, s, a, rows, first, dweight, dbias);
+            else hipLaunchKernelGGL((layer_norm_bwd_small_kernel<false>), dim3(n), dim3(1024), 0, s, a, rows, first, dweight, dbias);
+        };
+        if (ds != dy) {
+            go(0, rows + cols);
+        } else {   // the columns' sums before dy is written over
+            go(rows, cols);
+            go(0, rows);
+        }
+        return hipGetLastError();
+    }
     if (bf) launch_bwd<true>(a, p, s);
     else launch_bwd<false>(a, p, s);
     hipLaunchKernelGGL(layer_norm_reduce_kernel, dim3((dbias ? 2 : 1) * d / 64), dim3(1024), 0, s, part, p.blocks, d,

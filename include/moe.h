@@ -600,6 +600,103 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
                          float* dw_router, void* ws, size_t ws_bytes, void* stream, const float* dlogits_aux,
                          const uint8_t* xq);
 
+/* ---------------------------------------------------------------- the optimizer's step
+ *
+ * The norm of the gradients of many tensors, and an AdamW step over them, each
+ * in one launch for all tensors of the same types: the end of a training step
+ * whose gradients moe_backward and the norms' backward leave in float32.  With
+ * t the number of the step and factor the clipping factor (1 without):
+ *   g' = factor g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   w = w - lr lr_scale (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay w)
+ * in float32, per element.
+ *
+ * moe_param, one tensor of n elements (contiguous, any shape; n = 0 is passed
+ * over).  Device pointers, 16-byte aligned:
+ *   weight  : [n] w_dtype (MOE_F32 or MOE_BF16), in and out; NULL with master,
+ *             m, v and the scales: a gradient for moe_grad_norm only
+ *   grad    : [n] g_dtype (MOE_F32 or MOE_BF16)
+ *   master  : [n] float32, in and out, or NULL.  For MOE_BF16 weights: the step
+ *             is made on it and weight is its nearest bfloat16.  A MOE_BF16
+ *             weight without it is rounded stochastically (below)
+ *   m, v    : [n] moments, in and out, zero before the first step.  Without
+ *             scales float32.  With m_scale and v_scale ([ceil(n / 128)] float32)
+ *             8 bits an element: E4M3 codes whose values, times the scale of
+ *             their 128 consecutive elements, are m and sqrt(v)
+ *
+ * 8-bit moments: a block's scale is amax / 448 (amax over its finite values; 0
+ * for a block below 2^-100); a value x has the E4M3 code floor(c + f + (r + 1/2) / 2^16)
+ * with its sign, at most 126, for c the code at or below 448 |x| / amax, f the
+ * part of the way to the next code's value and r the low (m) or high (v) 16 bits of
+ *   mix(K + i 0x9E3779B9),  K = mix(mix(mix(mix(t) ^ seed) + tensor) ^ block),
+ * i the element's place in its block, tensor the place in the list, mix the
+ * 32-bit finalizer of MurmurHash3.  Infinite and NaN values have the NaN code.
+ * A MOE_BF16 weight without master: its float32 bits plus the low 16 bits of
+ * mix(that number + 0x7F4A7C15), cut to bfloat16.
+ *
+ * moe_param_table: writes the table that the calls read, moe_param_table_bytes()
+ * bytes, to host memory and describes it in *plan (host only, no GPU call).  The
+ * caller copies it to device memory, 16-byte aligned, before the first call and
+ * keeps it, and the tensors where they are, as long as calls use it.  The calls
+ * keep counters and partial sums in it: calls that share a table must not
+ * overlap.  Errors: MOE_ERR_NULL (params, a grad, weight without m or v or the
+ * reverse, one scale without the other), MOE_ERR_DTYPE (types; a master for
+ * MOE_F32 weights), MOE_ERR_SHAPE (count < 1, n < 0, n >= 2^38, 2^43 elements in
+ * all), MOE_ERR_ARG (not aligned, an infinite or NaN lr_scale or weight_decay,
+ * tensors that a step writes overlapping any other), MOE_ERR_WORKSPACE
+ * (table_bytes; host memory).
+ *
+ * moe_grad_norm: norm_clip[0] = sqrt(sum of squares of all gradients), in
+ * float64, norm_clip[1] = max_norm / norm where the norm is larger than max_norm
+ * (> 0, may be infinite), else 1; NaN if the norm is infinite or NaN.  Sums run
+ * in a fixed order (bitwise reproducible).
+ *   norm_clip : device float32 [2] out
+ *
+ * moe_adamw: one step of every tensor.
+ *   hyper : host; betas in [0, 1), eps >= 0, seed of the random bits
+ *   lr    : device float32 [1]
+ *   clip  : device float32 [2] as moe_grad_norm writes it, or NULL.  If the
+ *           factor is infinite or NaN the step is left out: nothing changes
+ *   step  : device int32 [2], in and out: the number of steps taken, which the
+ *           call counts up, and a counter that is 0 between calls.  Zero before
+ *           the first step
+ * A replayed graph takes the next step each time.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_ARG (betas, eps, max_norm, alignment), MOE_ERR_STATE (a plan that
+ * moe_param_table did not write, for moe_adamw also one with gradients alone). */
+typedef struct moe_param {
+    void* weight;
+    const void* grad;
+    float* master;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    int64_t n;
+    int32_t w_dtype;
+    int32_t g_dtype;
+    float lr_scale;
+    float weight_decay;
+} moe_param;
+
+typedef struct moe_param_plan {
+    int32_t first[14];      /* chunks of each kind of tensor begin here */
+    uint32_t check;
+    uint64_t descs, map;    /* offsets in the table */
+    uint64_t table_bytes;
+} moe_param_plan;
+
+typedef struct moe_adamw_hyper {
+    double beta1, beta2;
+    float eps;
+    uint32_t seed;
+} moe_adamw_hyper;
+
+int32_t moe_param_table_bytes(const moe_param* params, int32_t count, size_t* bytes);
+int32_t moe_param_table(const moe_param* params, int32_t count, void* host_table, size_t table_bytes,
+                        moe_param_plan* plan);
+int32_t moe_grad_norm(const moe_param_plan* plan, void* table, float max_norm, float* norm_clip, void* stream);
+int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper* hyper, const float* lr,
+                  const float* clip, int32_t* step, void* stream);
+
 /* ---------------------------------------------------------------- a few tokens (serving)
  *
  * The block for up to MOE_DECODE_MAX_TOKENS tokens with 4-bit expert weights:

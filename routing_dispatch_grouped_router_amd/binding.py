@@ -29,6 +29,7 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_packe
            "moe_pack_weights_backward", "moe_backward", "moe_set_test_flags", "moe_route_noalloc",
            "moe_fused_status", "moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward",
            "moe_layer_norm", "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
+           "moe_param_table_bytes", "moe_param_table", "moe_grad_norm", "moe_adamw",
            "moe_forward_quantized", "moe_balance_workspace_bytes", "moe_balance_loss",
            "moe_balance_loss_backward", "moe_router_backward_workspace_bytes", "moe_router_backward",
            "moe_backward_aux_workspace_bytes", "moe_backward_aux", "moe_decode_weight_bytes",
@@ -50,6 +51,22 @@ class Problem(ctypes.Structure):
     @property
     def act(self) -> str:
         return {v: k for k, v in ACT.items()}[self.act_dtype]
+
+
+class Param(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("weight", "grad", "master", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32),
+        ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class ParamPlan(ctypes.Structure):
+    _fields_ = [("first", ctypes.c_int32 * 14), ("check", ctypes.c_uint32), ("descs", ctypes.c_uint64),
+                ("map", ctypes.c_uint64), ("table_bytes", ctypes.c_uint64)]
+
+
+class AdamwHyper(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float),
+                ("seed", ctypes.c_uint32)]
 
 
 def problem(T, d, E, k, H, act, logits_given=False, identity=False, keep_gate_up=False) -> Problem:
@@ -102,6 +119,10 @@ def lib():
         L.moe_norm_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_layer_norm.argtypes = [PP, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P]
         L.moe_layer_norm_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_param_table_bytes.argtypes = [ctypes.POINTER(Param), _I32, ctypes.POINTER(_SZ)]
+        L.moe_param_table.argtypes = [ctypes.POINTER(Param), _I32, _P, _SZ, ctypes.POINTER(ParamPlan)]
+        L.moe_grad_norm.argtypes = [ctypes.POINTER(ParamPlan), _P, ctypes.c_float, _P, _P]
+        L.moe_adamw.argtypes = [ctypes.POINTER(ParamPlan), _P, ctypes.POINTER(AdamwHyper), _P, _P, _P, _P]
         L.moe_forward_quantized.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_balance_loss.argtypes = [PP, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_balance_loss_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P]
@@ -717,6 +738,173 @@ class RouterBackward(_Operator):
             self._p, *_inputs(self._index, dlogits, x, w_router, dx_in), _own(self.dx), _own(self.dw_router),
             _own(self.ws) if self.ws.numel() else None, self.ws.numel(), _stream(stream, self._index)))
         return dict(dx=self.dx, dw_router=self.dw_router)
+
+
+class _Params:
+    """A table of tensors on the device (moe_param_table), and the tensors, which have
+    to stay where they are: an optimizer's, updated in place."""
+
+    def __init__(self, grads, weights=None, **more):
+        """more: lists like grads of the fields of a moe_param."""
+        self.grads = tuple(grads)
+        if not self.grads:
+            raise ValueError("grads: expected at least one tensor")
+        self._device = self.grads[0].device
+        self._index = self.grads[0].get_device()
+        self.norm = torch.empty((2,), dtype=torch.float32, device=self._device)
+        n = len(self.grads)
+        fields = dict(grad=self.grads, weight=weights, **more)
+        params = (Param * n)()
+        for i, p in enumerate(params):
+            p.n, p.g_dtype = self.grads[i].numel(), _param_type(self.grads[i], "grads")
+            if weights is not None:
+                if weights[i].shape != self.grads[i].shape:
+                    raise ValueError(f"grads: expected {tuple(weights[i].shape)}, got {tuple(self.grads[i].shape)}")
+                p.w_dtype = _param_type(weights[i], "weights")
+            for name, values in fields.items():
+                if values is None:
+                    continue
+                value = values[i]
+                if isinstance(value, torch.Tensor):
+                    if value.device != self._device:
+                        raise ValueError(f"{name} is on {value.device}, expected {self._device}")
+                    value = _ptr(value)
+                setattr(p, name, value)
+        size, self._plan = _SZ(), ParamPlan()
+        _check("moe_param_table_bytes", lib().moe_param_table_bytes(params, n, ctypes.byref(size)))
+        host = torch.empty(size.value, dtype=torch.uint8)
+        _check("moe_param_table", lib().moe_param_table(params, n, host.data_ptr(), size.value,
+                                                        ctypes.byref(self._plan)))
+        self._table = host.to(self._device)
+        torch.cuda.current_stream(self._device).synchronize()   # the calls may run on other streams
+        self._plan_p, self._table_p, self._norm_p = ctypes.byref(self._plan), _own(self._table), _own(self.norm)
+
+    def _on_device(self):
+        if torch.cuda.current_device() != self._index:
+            raise ValueError(f"the tensors are on cuda:{self._index}, the current device is cuda:{torch.cuda.current_device()}")
+
+    def grad_norm(self, max_norm: float = float("inf"), stream=None):
+        """norm [2]: the norm of all gradients together, and the factor that brings it to max_norm
+        at most (NaN where the norm is not finite)."""
+        self._on_device()
+        _check("moe_grad_norm", lib().moe_grad_norm(self._plan_p, self._table_p, max_norm, self._norm_p,
+                                                    _stream(stream, self._index)))
+        return self.norm
+
+
+def _param_type(t, name):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+
+
+class GradNorm(_Params):
+    """The norm of many gradients (float32 or bfloat16 tensors, which stay where they are)."""
+
+    def __init__(self, grads):
+        super().__init__(grads)
+
+    __call__ = _Params.grad_norm
+
+
+class AdamW(_Params):
+    """An AdamW step over many tensors at once (moe_adamw), their moments and step count.
+
+    weights, grads: lists of tensors of the same shapes (float32 or bfloat16 each), which stay
+    where they are; the step updates the weights in place.
+    lr: a number, or a float32 tensor [1]; self.lr is that tensor, which a schedule writes to.
+    weight_decay, lr_scale: a number, or one for each tensor.
+    master: float32 copies of bfloat16 weights that the step is made on: a list (None in a float32
+    weight's place), True: made here, None: bfloat16 weights are rounded stochastically.
+    states: "f32": moments m and v, or "8bit": codes m and r (of v's root) with scales m_scale and
+    r_scale.  They, and step [2], are made here, zero, unless given (a checkpoint's).
+    seed: of the random bits that bfloat16 weights without master and 8-bit moments are rounded with."""
+
+    def __init__(self, weights, grads, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, lr_scale=1.0,
+                 master=None, states: str = "f32", seed: int = 0, step=None, m=None, v=None, r=None, m_scale=None,
+                 r_scale=None):
+        weights = tuple(weights)
+        if len(weights) != len(tuple(grads)) or not weights:
+            raise ValueError(f"expected as many grads as weights, got {len(tuple(grads))} and {len(weights)}")
+        if states not in ("f32", "8bit"):
+            raise ValueError(f"states: expected 'f32' or '8bit', got {states!r}")
+        device, eight = weights[0].device, states == "8bit"
+        if eight and v is not None or not eight and (r is not None or m_scale is not None or r_scale is not None):
+            raise ValueError("8-bit states are m, r, m_scale and r_scale, others m and v")
+        self.weights, self.states = weights, states
+
+        def many(name, given, dtype, count):
+            """A list of tensors like the weights', `given` or zero."""
+            if given is None:
+                return [torch.zeros((count(w.numel()),) if count else w.shape, dtype=dtype, device=device) for w in weights]
+            given = list(given)
+            if len(given) != len(weights):
+                raise ValueError(f"{name}: expected {len(weights)} tensors, got {len(given)}")
+            for t, w in zip(given, weights):
+                _expect(t, (count(w.numel()),) if count else w.shape, dtype, name)
+            return given
+
+        def blocks(n):
+            return (n + 127) // 128
+        moment = torch.uint8 if eight else torch.float32
+        self.m = many("m", m, moment, None)
+        self.m_scale = self.r_scale = self.v = self.r = None
+        if eight:
+            self.r = many("r", r, moment, None)
+            self.m_scale, self.r_scale = many("m_scale", m_scale, torch.float32, blocks), many("r_scale", r_scale, torch.float32, blocks)
+        else:
+            self.v = many("v", v, moment, None)
+        if master is True:
+            master = [w.float() if w.dtype == torch.bfloat16 else None for w in weights]
+        if master is not None:
+            master = list(master)
+            if len(master) != len(weights):
+                raise ValueError(f"master: expected {len(weights)}, got {len(master)}")
+            for t, w in zip(master, weights):
+                if t is not None:
+                    _expect(t, w.shape, torch.float32, "master")
+        self.master = master
+        if not isinstance(lr, torch.Tensor):
+            lr = torch.full((1,), float(lr), dtype=torch.float32, device=device)
+        _expect(lr, (1,), torch.float32, "lr")
+        step = torch.zeros((2,), dtype=torch.int32, device=device) if step is None else step
+        _expect(step, (2,), torch.int32, "step")
+        self._lr, self._step = lr, step
+
+        def each(name, value):
+            value = list(value) if isinstance(value, (list, tuple)) else [value] * len(weights)
+            if len(value) != len(weights):
+                raise ValueError(f"{name}: expected {len(weights)} numbers, got {len(value)}")
+            return [float(x) for x in value]
+        super().__init__(grads, weights, master=master, m=self.m, v=self.r if eight else self.v, m_scale=self.m_scale,
+                         v_scale=self.r_scale, weight_decay=each("weight_decay", weight_decay),
+                         lr_scale=each("lr_scale", lr_scale))
+        for name, t in (("lr", lr), ("step", step)):
+            if t.device != self._device:
+                raise ValueError(f"{name} is on {t.device}, expected {self._device}")
+        self._hyper = AdamwHyper(float(betas[0]), float(betas[1]), float(eps), int(seed) & 0xFFFFFFFF)
+        self._hyper_p, self._lr_p, self._step_p = ctypes.byref(self._hyper), _ptr(lr), _ptr(step)
+
+    @property
+    def lr(self):
+        return self._lr
+
+    @property
+    def step(self):
+        """int32 [2]: the number of steps taken, and a counter of the kernel's."""
+        return self._step
+
+    def __call__(self, clip=None, stream=None):
+        """One step.  clip: grad_norm's result, whose factor the gradients are multiplied with; the step is
+        left out if that is not finite."""
+        if clip is not None and clip is not self.norm:
+            _expect(clip, (2,), torch.float32, "clip")
+            if clip.device != self._device:
+                raise ValueError(f"clip is on {clip.device}, expected {self._device}")
+        self._on_device()
+        _check("moe_adamw", lib().moe_adamw(self._plan_p, self._table_p, self._hyper_p, self._lr_p,
+                                            None if clip is None else _ptr(clip), self._step_p,
+                                            _stream(stream, self._index)))
 
 
 MOE_DECODE_MAX_TOKENS = 256

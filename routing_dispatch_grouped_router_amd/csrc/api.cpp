@@ -10,9 +10,11 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "moe.h"
 #include "moe_internal.h"
+#include "params.h"
 
 using namespace moe;
 
@@ -255,6 +257,92 @@ DecodeLayout decode_layout(const moe_problem& p) {
     L.rwt = take(!(p.flags & MOE_LOGITS_GIVEN) && E % 8 ? E * d * 2 : 0);   // router W^T
     L.total = off;
     return L;
+}
+
+// ------------------------------------------------------------------ tables of parameters
+
+constexpr uint32_t kPlanCheck = 0x504C414Eu;
+
+int64_t param_chunks(int64_t n) { return (n + kParamChunk - 1) / kParamChunk; }
+
+int32_t check_param(const moe_param& p) {
+    if (p.n < 0 || p.n >= (int64_t)1 << 38) return MOE_ERR_SHAPE;
+    auto type = [](int32_t t) { return t == MOE_F32 || t == MOE_BF16; };
+    const bool trained = p.weight != nullptr;
+    if (!type(p.g_dtype) || (trained && (!type(p.w_dtype) || (p.master && p.w_dtype != MOE_BF16)))) return MOE_ERR_DTYPE;
+    if (!std::isfinite(p.lr_scale) || !std::isfinite(p.weight_decay)) return MOE_ERR_ARG;
+    if (p.n == 0) return MOE_OK;   // an empty tensor has no address
+    if (!p.grad || (!p.m_scale) != (!p.v_scale)) return MOE_ERR_NULL;
+    if (trained ? !p.m || !p.v : p.master || p.m || p.v || p.m_scale) return MOE_ERR_NULL;
+    for (const void* q : {p.weight, (void*)p.grad, (void*)p.master, p.m, p.v, (void*)p.m_scale, (void*)p.v_scale})
+        if (off_by(q, 16)) return MOE_ERR_ARG;
+    return MOE_OK;
+}
+
+int param_kind(const moe_param& p) {
+    if (!p.weight) return kKindNorm;
+    const int w = p.w_dtype == MOE_F32 ? 0 : (p.master ? 1 : 2);
+    return 4 * w + 2 * (p.m_scale != nullptr) + (p.g_dtype == MOE_BF16);
+}
+
+struct ParamLayout {
+    int64_t chunks, live;      // live: tensors with elements
+    size_t descs, map, total;
+};
+
+int32_t param_layout(const moe_param* params, int32_t count, ParamLayout* L) {
+    if (!params) return MOE_ERR_NULL;
+    if (count < 1) return MOE_ERR_SHAPE;
+    *L = {};
+    for (int32_t i = 0; i < count; ++i) {
+        const int32_t st = check_param(params[i]);
+        if (st) return st;
+        L->chunks += param_chunks(params[i].n);
+        L->live += params[i].n > 0;
+    }
+    if (L->chunks > INT_MAX) return MOE_ERR_SHAPE;
+    L->descs = align256(sizeof(ParamHead));
+    L->map = L->descs + align256(L->live * sizeof(ParamDesc));
+    L->total = L->map + align256(L->chunks * sizeof(uint32_t));
+    return MOE_OK;
+}
+
+struct Span {
+    uintptr_t begin, end;
+    bool written;
+};
+
+// Whether a tensor that the step writes overlaps another one.
+int32_t check_spans(const moe_param* params, int32_t count) {
+    Span* spans = new (std::nothrow) Span[(size_t)count * 7];
+    if (!spans) return MOE_ERR_WORKSPACE;
+    size_t n = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const moe_param& p = params[i];
+        if (p.n == 0) continue;
+        auto add = [&](const void* q, int64_t bytes, bool written) {
+            const uintptr_t b = reinterpret_cast<uintptr_t>(q);
+            if (q) spans[n++] = {b, b + (uintptr_t)bytes, written};
+        };
+        const int64_t moment = p.m_scale ? 1 : 4, scales = (p.n + kParamBlock - 1) / kParamBlock * 4;
+        add(p.weight, p.n * (p.w_dtype == MOE_F32 ? 4 : 2), true);
+        add(p.grad, p.n * (p.g_dtype == MOE_F32 ? 4 : 2), false);
+        add(p.master, p.n * 4, true);
+        add(p.m, p.n * moment, true);
+        add(p.v, p.n * moment, true);
+        add(p.m_scale, scales, true);
+        add(p.v_scale, scales, true);
+    }
+    std::sort(spans, spans + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    uintptr_t end = 0, end_written = 0;
+    bool clash = false;
+    for (size_t i = 0; i < n; ++i) {
+        clash |= spans[i].begin < (spans[i].written ? end : end_written);
+        end = std::max(end, spans[i].end);
+        if (spans[i].written) end_written = std::max(end_written, spans[i].end);
+    }
+    delete[] spans;
+    return clash ? MOE_ERR_ARG : MOE_OK;
 }
 
 // ------------------------------------------------------------------ profiling (moe_forward only)
@@ -1077,6 +1165,83 @@ int32_t moe_router_backward(const moe_problem* p, const float* dlogits, const vo
         return st;
     return launched(launch_router_dw(p->act_dtype, dlogits, x, static_cast<float*>(ws), dw_router, p->T, p->d_model,
                                      p->n_experts, s));
+}
+
+// ----------------------------------------------------------------------------- the optimizer's step
+
+int32_t moe_param_table_bytes(const moe_param* params, int32_t count, size_t* bytes) {
+    ParamLayout L;
+    const int32_t st = param_layout(params, count, &L);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = L.total;
+    return MOE_OK;
+}
+
+int32_t moe_param_table(const moe_param* params, int32_t count, void* host_table, size_t table_bytes,
+                        moe_param_plan* plan) {
+    ParamLayout L;
+    int32_t st = param_layout(params, count, &L);
+    if (st) return st;
+    if (!host_table || !plan) return MOE_ERR_NULL;
+    if (table_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if ((st = check_spans(params, count))) return st;
+    memset(host_table, 0, L.total);
+    ParamDesc* descs = reinterpret_cast<ParamDesc*>(at(host_table, L.descs));
+    uint32_t* map = reinterpret_cast<uint32_t*>(at(host_table, L.map));
+    moe_param_plan out{};
+    uint32_t d = 0, c = 0;
+    for (int kind = 0; kind <= kKindNorm; ++kind) {
+        out.first[kind] = (int32_t)c;
+        for (int32_t i = 0; i < count; ++i) {
+            const moe_param& p = params[i];
+            if (p.n == 0 || param_kind(p) != kind) continue;
+            descs[d] = {p.weight, p.grad, p.master, p.m, p.v, p.m_scale, p.v_scale, (uint64_t)p.n, p.lr_scale,
+                        p.weight_decay, (uint32_t)i, c, p.g_dtype == MOE_BF16, 0};
+            for (int64_t k = param_chunks(p.n); k > 0; --k) map[c++] = d;
+            ++d;
+        }
+    }
+    out.first[kKindNorm + 1] = (int32_t)c;
+    out.check = kPlanCheck;
+    out.descs = L.descs;
+    out.map = L.map;
+    out.table_bytes = L.total;
+    *plan = out;
+    return MOE_OK;
+}
+static_assert(sizeof(moe_param_plan::first) / sizeof(int32_t) == kKindNorm + 2, "one entry for every kind, and the end");
+
+int32_t moe_grad_norm(const moe_param_plan* plan, void* table, float max_norm, float* norm_clip, void* stream) {
+    if (!plan || !table || !norm_clip) return MOE_ERR_NULL;
+    if (plan->check != kPlanCheck) return MOE_ERR_STATE;
+    if (!(max_norm > 0.f) || off_by(table, 16) || off_by(norm_clip, 4)) return MOE_ERR_ARG;
+    return launched(launch_grad_norm(table, plan->descs, plan->map, plan->first[kKindNorm + 1], max_norm, norm_clip,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper* hyper, const float* lr,
+                  const float* clip, int32_t* step, void* stream) {
+    if (!plan || !table || !hyper || !lr || !step) return MOE_ERR_NULL;
+    if (plan->check != kPlanCheck || plan->first[kKindNorm] != plan->first[kKindNorm + 1]) return MOE_ERR_STATE;
+    auto beta = [](double b) { return b >= 0.0 && b < 1.0; };
+    if (!beta(hyper->beta1) || !beta(hyper->beta2) || !(hyper->eps >= 0.f) || !std::isfinite(hyper->eps) ||
+        off_by(table, 16) || off_by(lr, 4) || off_by(clip, 4) || off_by(step, 4))
+        return MOE_ERR_ARG;
+    AdamArgs a{static_cast<const unsigned char*>(table), plan->descs, plan->map, 0, 0, lr, clip, step, 0, hyper->seed,
+               hyper->beta1, hyper->beta2, hyper->eps};
+    int last = 0;   // the last kind with tensors counts the step
+    for (int kind = 0; kind < kKinds; ++kind)
+        if (plan->first[kind] < plan->first[kind + 1]) last = kind;
+    for (int kind = 0; kind <= last; ++kind) {
+        a.first = plan->first[kind];
+        a.end = plan->first[kind + 1];
+        a.count = kind == last;
+        if (a.first == a.end && !a.count) continue;
+        const int32_t st = launched(launch_adamw(kind, a, static_cast<hipStream_t>(stream)));
+        if (st) return st;
+    }
+    return MOE_OK;
 }
 
 // ----------------------------------------------------------------------------- a few tokens, 4-bit weights

@@ -259,6 +259,15 @@ hipError_t launch_layer_norm_bwd(int act, const void* dy, const void* dsum, cons
                                  const float* mean, const float* rstd, void* ds, float* dweight, float* dbias,
                                  float* part, int T, int d, hipStream_t s);
 
+// ---------------------------------------------------------------- gradients' norm, AdamW (adamw.hip)
+
+struct AdamArgs;   // params.h
+// The chunks [first, end) of the table, all of one kind.
+hipError_t launch_adamw(int kind, const AdamArgs& a, hipStream_t s);
+// out[0] = norm of all gradients of the table, out[1] = the factor that brings it to max_norm at most.
+hipError_t launch_grad_norm(void* table, size_t descs, size_t map, int chunks, float max_norm, float* out,
+                            hipStream_t s);
+
 // ---------------------------------------------------------------- balance loss (balance.hip)
 
 // Scratch of the forward: part holds this many float, cnt as many int32.

@@ -656,9 +656,8 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  *   lr    : device float32 [1]
  *   clip  : device float32 [2] as moe_grad_norm writes it, or NULL.  If the
  *           factor is infinite or NaN the step is left out: nothing changes
- *   step  : device int32 [2], in and out: the number of steps taken, which the
- *           call counts up, and a counter that is 0 between calls.  Zero before
- *           the first step
+ *   step  : device int32 [2], in and out: the number of steps taken, zero before
+ *           the first, which the call counts up; the second word is not touched
  * A replayed graph takes the next step each time.  Errors: MOE_ERR_NULL,
  * MOE_ERR_ARG (betas, eps, max_norm, alignment), MOE_ERR_STATE (a plan that
  * moe_param_table did not write, for moe_adamw also one with gradients alone). */

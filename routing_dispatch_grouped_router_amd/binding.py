@@ -891,7 +891,7 @@ class AdamW(_Params):
 
     @property
     def step(self):
-        """int32 [2]: the number of steps taken, and a counter of the kernel's."""
+        """int32 [2]: the number of steps taken, and a word that is not touched."""
         return self._step
 
     def __call__(self, clip=None, stream=None):

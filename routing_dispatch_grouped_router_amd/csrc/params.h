@@ -13,7 +13,7 @@
 namespace moe {
 
 constexpr int kParamBlock = 128;       // elements of an 8-bit moment that share a scale
-constexpr int kParamChunk = 4096;
+constexpr int kParamChunk = 2048;      // eight elements a thread
 constexpr int kNormGroups = 1024;      // most workgroups of the norm, and partial sums
 
 // Kinds: 4 * (weights: 0 float32, 1 bfloat16 with a float32 master, 2 bfloat16 alone)
@@ -38,19 +38,28 @@ struct ParamDesc {
 };
 static_assert(sizeof(ParamDesc) == 88, "read by the kernels as it is written here");
 
+// Counters that find the last workgroup of a launch, zero between launches.  One
+// address takes an atomic of the whole card every 30 to 70 ns (1024 workgroups: 65
+// us), so workgroups count in 32 groups, each on a line of its own, and the
+// groups' last ones once more.
+struct Tickets {
+    uint32_t group[32][16];
+    uint32_t all[16];
+};
+
 struct ParamHead {
-    uint32_t norm_ticket, step_ticket;   // zero between calls
-    uint32_t pad[62];
+    Tickets norm, step;
     double part[kNormGroups];
 };
 
 struct AdamArgs {
-    const unsigned char* table;
+    unsigned char* table;
     size_t descs, map;     // offsets in the table
     int first, end;        // chunks of this launch
     const float* lr;       // [1]
     const float* clip;     // [2], the second used; NULL: 1
-    int32_t* step;         // [2]: steps taken; a counter
+    int32_t* step;         // [2]: steps taken; not used
+    bool nt;               // whether the tensors are streamed past the caches
     int count;             // whether this launch, the step's last, counts it
     uint32_t seed;
     double beta1, beta2;

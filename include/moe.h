@@ -640,7 +640,7 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  * keep counters and partial sums in it: calls that share a table must not
  * overlap.  Errors: MOE_ERR_NULL (params, a grad, weight without m or v or the
  * reverse, one scale without the other), MOE_ERR_DTYPE (types; a master for
- * MOE_F32 weights), MOE_ERR_SHAPE (count < 1, n < 0, n >= 2^38, 2^43 elements in
+ * MOE_F32 weights), MOE_ERR_SHAPE (count < 1, n < 0, n >= 2^38, 2^42 elements in
  * all), MOE_ERR_ARG (not aligned, an infinite or NaN lr_scale or weight_decay,
  * tensors that a step writes overlapping any other), MOE_ERR_WORKSPACE
  * (table_bytes; host memory).
@@ -695,6 +695,30 @@ int32_t moe_param_table(const moe_param* params, int32_t count, void* host_table
 int32_t moe_grad_norm(const moe_param_plan* plan, void* table, float max_norm, float* norm_clip, void* stream);
 int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper* hyper, const float* lr,
                   const float* clip, int32_t* step, void* stream);
+
+/* ---------------------------------------------------------------- a few tokens, packed weights
+ *
+ * moe_forward for up to MOE_FEW_MAX_TOKENS tokens on the same packed weights
+ * (moe_pack_weights'), read once for all rows of an expert: what a model under
+ * training is sampled and evaluated with.  Every act_dtype; MOE_MXFP8 blocks
+ * take x as it is (bfloat16, not quantised) and h is not quantised either; h of
+ * MOE_BF16 and MOE_MXFP8 blocks is held as two bfloat16 terms (2^-16 of it left
+ * out).  No MOE_IDENTITY_EXPERTS; MOE_KEEP_GATE_UP has no effect.
+ *   logits : device float32 [T, E]; input with MOE_LOGITS_GIVEN, else output
+ *   mask   : device uint8 [T] or NULL; 0: the token is padding, its row of x may
+ *            hold anything, its topk_idx are -1, its gates and its row of y 0
+ *   topk_idx [T, k], topk_gate [T, k] : out, or NULL (kept in the workspace)
+ *   y      : device [T, d] out (activation type, bfloat16 for MOE_MXFP8); may be x
+ *   ws     : moe_forward_few_workspace_bytes (host-only query)
+ * Ties and gates as moe_route; a token's result does not depend on the other
+ * tokens of the call.  x, w_router, logits, packed_w, y and ws are 16-byte aligned.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T over the limit too), MOE_ERR_DTYPE,
+ * MOE_ERR_WORKSPACE, MOE_ERR_ARG for an unaligned pointer. */
+#define MOE_FEW_MAX_TOKENS 32
+int32_t moe_forward_few_workspace_bytes(const moe_problem* p, size_t* bytes);
+int32_t moe_forward_few(const moe_problem* p, const void* x, const void* w_router, float* logits, const void* packed_w,
+                        const uint8_t* mask, void* y, int32_t* topk_idx, float* topk_gate, void* ws, size_t ws_bytes,
+                        void* stream);
 
 /* ---------------------------------------------------------------- a few tokens (serving)
  *

@@ -33,7 +33,8 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_packe
            "moe_forward_quantized", "moe_balance_workspace_bytes", "moe_balance_loss",
            "moe_balance_loss_backward", "moe_router_backward_workspace_bytes", "moe_router_backward",
            "moe_backward_aux_workspace_bytes", "moe_backward_aux", "moe_decode_weight_bytes",
-           "moe_decode_workspace_bytes", "moe_pack_weights_decode", "moe_decode_experts", "moe_decode"]
+           "moe_decode_workspace_bytes", "moe_pack_weights_decode", "moe_decode_experts", "moe_decode",
+           "moe_forward_few_workspace_bytes", "moe_forward_few"]
 
 
 class MoeError(RuntimeError):
@@ -113,7 +114,7 @@ def lib():
         L.moe_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P,
                                    _P, _SZ, _P]
         for name in ("norm_backward_workspace", "layer_norm_backward_workspace", "balance_workspace", "router_backward_workspace",
-                     "backward_aux_workspace", "decode_weight", "decode_workspace"):
+                     "backward_aux_workspace", "decode_weight", "decode_workspace", "forward_few_workspace"):
             getattr(L, f"moe_{name}_bytes").argtypes = [PP, ctypes.POINTER(_SZ)]
         L.moe_norm.argtypes = [PP, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P]
         L.moe_norm_backward.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
@@ -131,6 +132,7 @@ def lib():
         L.moe_pack_weights_decode.argtypes = [PP, _P, _P, _P, _P, _P]
         L.moe_decode_experts.argtypes = [PP, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_decode.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_forward_few.argtypes = [PP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.moe_kernel_times.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float),
                                        _I32, ctypes.POINTER(_I32)]
         for name in EXPORTS:
@@ -965,6 +967,44 @@ class Decode(_Operator):
         _expect(packed, (self.weight_bytes,), torch.uint8, "packed")
         _check("moe_decode_experts", lib().moe_decode_experts(
             self._p, *_inputs(self._index, x, idx, gate, packed), _own(self.y), _own(self.ws),
+            self.ws.numel(), _stream(stream, self._index)))
+        return self.y
+
+
+MOE_FEW_MAX_TOKENS = 32
+
+
+class ForwardFew(_Operator):
+    """Preallocated outputs and workspace of the block for a few tokens on packed
+    weights (moe_forward_few): y [T, d], logits [T, E], idx and gate [T, k]."""
+
+    def __init__(self, p: Problem, device):
+        super().__init__(p, device)
+        self._shape, self._dt = _rows(p)
+        self._choices, self._router = (p.T, p.n_experts), (p.d_model, p.n_experts)
+        self.weight_bytes = packed_weight_bytes(p)
+        self._buffer("ws", (_bytes("moe_forward_few_workspace_bytes", p),), torch.uint8)
+        self._buffer("y", self._shape, self._dt)
+        self._buffer("logits", self._choices, torch.float32)
+        self._buffer("idx", (p.T, p.top_k), torch.int32)
+        self._buffer("gate", (p.T, p.top_k), torch.float32)
+
+    def __call__(self, x, packed, w_router=None, logits=None, mask=None, stream=None):
+        """The block on pack_weights' weights; mask (uint8 [T], None: all): tokens that are not
+        padding.  With given logits they are an argument, else self.logits is written.  Returns y."""
+        p = self.p
+        _expect(x, self._shape, self._dt, "x")
+        _expect(packed, (self.weight_bytes,), torch.uint8, "packed")
+        if p.flags & MOE_LOGITS_GIVEN:
+            _expect(logits, self._choices, torch.float32, "logits")
+        else:
+            _expect(w_router, self._router, self._dt, "w_router")
+            logits = self.logits
+        if mask is not None:
+            _expect(mask, self._shape[:1], torch.uint8, "mask")
+        x, w_router, logits, packed, mask = _inputs(self._index, x, w_router, logits, packed, mask)
+        _check("moe_forward_few", lib().moe_forward_few(
+            self._p, x, w_router, logits, packed, mask, _own(self.y), _own(self.idx), _own(self.gate), _own(self.ws),
             self.ws.numel(), _stream(stream, self._index)))
         return self.y
 

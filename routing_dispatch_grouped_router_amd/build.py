@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["route.hip", "dispatch.hip", "gemm.hip", "gemm_pipe.hip", "pack.hip", "backward.hip", "norm.hip",
-           "layer_norm.hip", "adamw.hip", "balance.hip", "router_bwd.hip", "decode.hip", "api.cpp"]
+           "layer_norm.hip", "adamw.hip", "balance.hip", "router_bwd.hip", "decode.hip", "few.hip", "api.cpp"]
 ARCH = "gfx950"
 
 

@@ -240,6 +240,33 @@ Packed decode_packed(const moe_problem& p) {
     return P;
 }
 
+// Problems of the block for a few tokens on packed weights.
+int32_t check_few(const moe_problem* p) {
+    int32_t st = check_problem(p);
+    if (st) return st;
+    if (p->flags & MOE_IDENTITY_EXPERTS) return MOE_ERR_DTYPE;
+    return p->T > MOE_FEW_MAX_TOKENS ? MOE_ERR_SHAPE : MOE_OK;
+}
+static_assert(kFewTokens == MOE_FEW_MAX_TOKENS, "the header's limit");
+
+struct FewLayout {
+    size_t h, idx, gate, rwt, total;
+};
+
+FewLayout few_layout(const moe_problem& p) {
+    FewLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) { size_t o = off; off += align256(bytes); return o; };
+    const size_t R = (size_t)p.T * p.top_k;
+    L.h = take(R * p.d_hidden * 4);   // float32, or two bfloat16 terms
+    L.idx = take(R * 4);
+    L.gate = take(R * 4);
+    L.rwt = take(!(p.flags & MOE_LOGITS_GIVEN) && !few_routes_itself(p.act_dtype, p.d_model, p.n_experts)
+                     ? (size_t)p.n_experts * p.d_model * 2 : 0);   // router W^T
+    L.total = off;
+    return L;
+}
+
 struct DecodeLayout {
     size_t h, ye, idx, gate, sel, rwt, total;
 };
@@ -1242,6 +1269,44 @@ int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper
         if (st) return st;
     }
     return MOE_OK;
+}
+
+// ----------------------------------------------------------------------------- a few tokens, packed weights
+
+int32_t moe_forward_few_workspace_bytes(const moe_problem* p, size_t* bytes) {
+    int32_t st = check_few(p);
+    if (st) return st;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = few_layout(*p).total;
+    return MOE_OK;
+}
+
+int32_t moe_forward_few(const moe_problem* p, const void* x, const void* w_router, float* logits, const void* packed_w,
+                        const uint8_t* mask, void* y, int32_t* topk_idx, float* topk_gate, void* ws, size_t ws_bytes,
+                        void* stream) {
+    int32_t st = check_few(p);
+    if (st) return st;
+    const bool given = p->flags & MOE_LOGITS_GIVEN;
+    if (!x || !logits || !packed_w || !y || !ws || (!given && !w_router)) return MOE_ERR_NULL;
+    if (off_by(x, 16) || off_by(w_router, 16) || off_by(logits, 16) || off_by(packed_w, 16) || off_by(y, 16) ||
+        off_by(topk_idx, 4) || off_by(topk_gate, 4) || off_by(ws, 16))
+        return MOE_ERR_ARG;
+    const FewLayout L = few_layout(*p);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    bool learned = !given;
+    if (learned && !few_routes_itself(p->act_dtype, p->d_model, p->n_experts)) {
+        if ((st = launched(launch_router_logits(p->act_dtype == MOE_F32 ? MOE_F32 : MOE_BF16, x, w_router, logits, p->T,
+                                                p->d_model, p->n_experts, reinterpret_cast<uint16_t*>(at(ws, L.rwt)), s))))
+            return st;
+        learned = false;
+    }
+    const Packed P = packed_layout(*p);
+    const uint8_t* pw = static_cast<const uint8_t*>(packed_w);
+    return launched(launch_few(p->act_dtype, x, w_router, learned, logits, mask, pw + P.w1, pw + P.w2, pw + P.s1, pw + P.s2, y,
+                               topk_idx ? topk_idx : reinterpret_cast<int32_t*>(at(ws, L.idx)),
+                               topk_gate ? topk_gate : reinterpret_cast<float*>(at(ws, L.gate)), at(ws, L.h), p->T,
+                               p->d_model, p->n_experts, p->top_k, p->d_hidden, s));
 }
 
 // ----------------------------------------------------------------------------- a few tokens, 4-bit weights

@@ -14,6 +14,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 16;
 // Most tokens of the decode form of the experts (MOE_DECODE_MAX_TOKENS).
 constexpr int kDecodeTokens = 256;
+// Most tokens of the block on packed weights for a few tokens (MOE_FEW_MAX_TOKENS).
+constexpr int kFewTokens = 32;
 
 enum Act { kF32 = 0, kBF16 = 1, kMXFP8 = 2 };
 
@@ -286,6 +288,15 @@ hipError_t launch_router_dx(int act, const float* dL, const void* w_router, cons
 size_t router_dw_part_bytes(int act, int T, int d, int E);
 hipError_t launch_router_dw(int act, const float* dL, const void* x, float* part, float* dw_router, int T, int d,
                             int E, hipStream_t s);
+
+// ---------------------------------------------------------------- few tokens, packed weights (few.hip)
+
+// Whether launch_few makes the logits of a learned router itself; else they are given (launch_router_logits).
+bool few_routes_itself(int act, int d, int E);
+// The block for T <= kFewTokens: logits (learned) or given ones, selection (mask [T] or NULL), experts.  h: T k H 4 bytes.
+hipError_t launch_few(int act, const void* x, const void* w_router, bool learned, float* logits, const uint8_t* mask,
+                      const uint8_t* w1, const uint8_t* w2, const uint8_t* s1, const uint8_t* s2, void* y, int32_t* idx,
+                      float* gate, void* h, int T, int d, int E, int k, int H, hipStream_t s);
 
 // ---------------------------------------------------------------- few tokens, 4-bit weights (decode.hip)
 

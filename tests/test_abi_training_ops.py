@@ -130,7 +130,7 @@ def test_param_table():
     st, plan, _ = _table(_param(n=5000), _param(w_dtype=1, master=0x150000, weight=0x110000, m=0x130000, v=0x140000),
                          _param(w_dtype=1, g_dtype=1, weight=0x210000, m=0x230000, v=0x240000, m_scale=0x250000, v_scale=0x260000, n=8193),
                          _param(weight=None, m=None, v=None), _param(n=0, weight=0, grad=0, m=0, v=0))
-    assert st == 0 and list(plan.first) == [0] + [2] * 4 + [3] * 7 + [6, 7]
+    assert st == 0 and list(plan.first) == [0] + [3] * 4 + [4] * 7 + [9, 10]
     assert _table(_param(n=(1 << 38) - 1), *[_param(weight=None, m=None, v=None, n=(1 << 38) - 1)] * 32)[0] == -2   # chunks
 
 
@@ -169,3 +169,36 @@ def test_adamw_binding():
         B.GradNorm([])
     with pytest.raises(ValueError, match="device tensor"):
         B.GradNorm([w])
+
+
+def test_forward_few():
+    name = "moe_forward_few"
+    _query(name + "_workspace_bytes", _p(T=32))
+    # x, w_router, logits, packed, mask, y, idx, gate, ws, ws_bytes, stream
+    ok = [F, F, F, F, None, G, None, None, F, BIG, None]
+    p, given = _p(T=8), _p(T=8, logits_given=True)
+    for i in (0, 1, 2, 3, 5, 8):
+        assert _call(name, p, *_swap(ok, i, None)) == -1
+    for i in (0, 2, 3, 5, 8):
+        assert _call(name, given, *_swap(_swap(ok, 1, None), i, None)) == -1
+    for i in (0, 1, 2, 3, 5, 8):
+        assert _call(name, p, *_swap(ok, i, ODD)) == -7
+    for i in (6, 7):
+        assert _call(name, p, *_swap(ok, i, ctypes.c_void_p(0x1002))) == -7
+    assert _call(name, p, *_swap(ok, 9, 64)) == -4
+    assert _call(name, _p(T=33), *ok) == -2 and _call(name, _p(T=8, d=96), *ok) == -2
+    assert _call(name, _p(T=8, act="mxfp8", H=192), *ok) == -2
+    assert _call(name, _p(T=8, identity=True), *ok) == -3
+
+
+def test_forward_few_binding(monkeypatch):
+    monkeypatch.setattr(B, "_inputs", lambda device, *t: [None if v is None else v.data_ptr() for v in t])
+    op = B.ForwardFew(_p(T=4), "cpu")
+    x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(256, 8, dtype=torch.bfloat16)
+    packed = torch.zeros(op.weight_bytes, dtype=torch.uint8)
+    for args, kw, match in (((x[:3], packed), dict(w_router=w), "x: expected"), ((x, packed[:5]), dict(w_router=w), "packed"),
+                            ((x, packed), {}, "w_router"), ((x, packed), dict(w_router=w, mask=torch.zeros(4)), "mask")):
+        with pytest.raises(ValueError, match=match):
+            op(*args, **kw)
+    with pytest.raises(ValueError, match="logits"):
+        B.ForwardFew(_p(T=4, logits_given=True), "cpu")(x, packed)

@@ -712,8 +712,9 @@ int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper
  *   ws     : moe_forward_few_workspace_bytes (host-only query)
  * Ties and gates as moe_route; a token's result does not depend on the other
  * tokens of the call.  x, w_router, logits, packed_w, y and ws are 16-byte aligned.
- * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T over the limit too), MOE_ERR_DTYPE,
- * MOE_ERR_WORKSPACE, MOE_ERR_ARG for an unaligned pointer. */
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T over the limit, T k max(d, H) float32 not
+ * below 2^32 bytes), MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an
+ * unaligned pointer. */
 #define MOE_FEW_MAX_TOKENS 32
 int32_t moe_forward_few_workspace_bytes(const moe_problem* p, size_t* bytes);
 int32_t moe_forward_few(const moe_problem* p, const void* x, const void* w_router, float* logits, const void* packed_w,

@@ -245,7 +245,10 @@ int32_t check_few(const moe_problem* p) {
     int32_t st = check_problem(p);
     if (st) return st;
     if (p->flags & MOE_IDENTITY_EXPERTS) return MOE_ERR_DTYPE;
-    return p->T > MOE_FEW_MAX_TOKENS ? MOE_ERR_SHAPE : MOE_OK;
+    // activations are addressed with 32-bit byte offsets, in their wider form
+    if (p->T > MOE_FEW_MAX_TOKENS || (long long)p->T * p->top_k * std::max(p->d_model, p->d_hidden) * 4 >= (1LL << 32))
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
 }
 static_assert(kFewTokens == MOE_FEW_MAX_TOKENS, "the header's limit");
 

@@ -168,85 +168,87 @@ struct ActPiece {
     u32x4 x[NT][TERMS][Seg<ACT>::kX];
 };
 
-// NB groups of 4 weight rows, row0[b] + the lane's, of an expert's [rows][K].
-template <int ACT, int NB>
-struct Weights {
-    const uint8_t* w[NB];
-    const uint8_t* s[NB];   // scales [K / 128][rows][4]
-    size_t slice;           // bytes of a 128-wide slice of them
-    int K;
-};
+// A uniform address plus a lane's 32-bit offset (an expert's weights and an
+// activation buffer are below 2^32 bytes).
+__device__ __forceinline__ u32x4 load16(const uint8_t* base, uint32_t off) {
+    return *reinterpret_cast<const u32x4*>(base + off);
+}
 
-template <int ACT, int NB>
-__device__ __forceinline__ Weights<ACT, NB> weights_at(const uint8_t* w, const uint8_t* s, const int (&row0)[NB], int rows,
-                                                       int K) {
-    const int lane = threadIdx.x & 63, a = (lane & 15) >> 2, p = 4 * (lane >> 4) + (lane & 3);
-    const size_t pitch = (size_t)K * (ACT == kF32 ? 4 : (ACT == kBF16 ? 2 : 1));
-    Weights<ACT, NB> o;
-    o.slice = (size_t)rows * 4;
-    o.K = K;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        o.w[b] = w + (size_t)(row0[b] + a) * pitch + 16 * p;
-        // piece p: elements 16 p .. of 256, scale (p / 2) % 4 of slice p / 8
-        o.s[b] = ACT == kMXFP8 ? s + (p >> 3) * o.slice + (size_t)(row0[b] + a) * 4 + ((p >> 1) & 3) : nullptr;
-    }
+__device__ __forceinline__ int lane_row() { return (threadIdx.x & 15) >> 2; }                              // a, or t
+__device__ __forceinline__ int lane_piece() { return 4 * ((threadIdx.x & 63) >> 4) + (threadIdx.x & 3); }   // p
+
+// Weights [experts][rows][K] (scales [experts][K / 128][rows][4]) as a lane reads them: piece p of weight row
+// row0 + 4 b + a of NB groups of 4 rows, `apart` rows from one group to the next.
+template <int ACT>
+struct Weights {
+    const uint8_t* w;       // of the expert
+    const uint8_t* s;
+    uint32_t wo, so;        // the lane's offsets in group 0
+};
+template <int ACT>
+constexpr int kWBytes = ACT == kF32 ? 4 : (ACT == kBF16 ? 2 : 1);
+
+template <int ACT>
+__device__ __forceinline__ Weights<ACT> weights_at(const uint8_t* w, const uint8_t* s, int e, int row0, int rows, int K) {
+    const size_t expert = (size_t)e * rows * K;
+    Weights<ACT> o;
+    o.w = w + expert * kWBytes<ACT>;
+    o.s = s + expert / 32;
+    o.wo = (uint32_t)(row0 + lane_row()) * (uint32_t)(K * kWBytes<ACT>) + 16 * lane_piece();
+    // piece p: elements 16 p .. of 256, scale (p / 2) % 4 of slice p / 8
+    o.so = ACT == kMXFP8 ? (uint32_t)(((lane_piece() >> 3) * rows + row0 + lane_row()) * 4 + ((lane_piece() >> 1) & 3)) : 0u;
     return o;
 }
 
-// Rows rows[n0 ..] (n in all) of activations x [.][TERMS][K], row r's line r / div; columns past the last row repeat it.
+// Offsets of rows rows[n0 ..] (n in all) of activations [.][TERMS][K], row r's line r / div; columns past the last row
+// repeat it.
 template <int ACT, int NT, int TERMS>
 struct Acts {
-    const uint8_t* x[NT];
-    uint32_t term;
+    uint32_t x[NT];
 };
 template <int ACT, int NT, int TERMS>
-__device__ __forceinline__ Acts<ACT, NT, TERMS> acts_at(const void* x, const uint16_t* rows, int n0, int n, int div, int K) {
-    const int lane = threadIdx.x & 63, t = (lane & 15) >> 2, p = 4 * (lane >> 4) + (lane & 3);
+__device__ __forceinline__ Acts<ACT, NT, TERMS> acts_at(const uint16_t* rows, int n0, int n, int div, int K) {
     Acts<ACT, NT, TERMS> o;
-    o.term = (uint32_t)K * (ACT == kF32 ? 4u : 2u);
+    const uint32_t term = (uint32_t)K * (ACT == kF32 ? 4u : 2u);
 #pragma unroll
-    for (int g = 0; g < NT; ++g) {
-        const int line = rows[min(n0 + 4 * g + t, n - 1)] / div;
-        o.x[g] = static_cast<const uint8_t*>(x) + (size_t)line * TERMS * o.term + (Seg<ACT>::kXBytes / 16) * p;
-    }
+    for (int g = 0; g < NT; ++g)
+        o.x[g] = (uint32_t)(rows[min(n0 + 4 * g + lane_row(), n - 1)] / div) * (TERMS * term) + (Seg<ACT>::kXBytes / 16) * lane_piece();
     return o;
 }
 
-// Whether this lane's piece of segment s is inside K (the last segment may be half of one).
-template <int ACT>
-__device__ __forceinline__ bool inside(int s, int K) {
-    return (s + 1) * Seg<ACT>::kElems <= K || (threadIdx.x & 63) < 32;
-}
-
-template <int ACT, int NB>
-__device__ __forceinline__ void load(const Weights<ACT, NB>& p, int s, WeightPiece<ACT, NB>& o) {
-    if (inside<ACT>(s, p.K)) {
+// Segment s of both (zero past K: the last segment may be half of one).  rows, K: the weights'; group b is `step(b)`
+// rows from the first.
+template <int ACT, int NB, int NT, int TERMS, typename Step>
+__device__ __forceinline__ void load(const Weights<ACT>& p, const uint8_t* x, const Acts<ACT, NT, TERMS>& in, int s,
+                                     int rows, int K, Step step, WeightPiece<ACT, NB>& w, ActPiece<ACT, NT, TERMS>& o) {
+    const bool inside = (s + 1) * Seg<ACT>::kElems <= K || (threadIdx.x & 63) < 32;
+    const uint32_t term = (uint32_t)K * (ACT == kF32 ? 4u : 2u);
+    if (inside) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            o.w[b] = *reinterpret_cast<const u32x4*>(p.w[b] + 256 * (size_t)s);
-            if (ACT == kMXFP8) o.sc[b] = p.s[b][2 * s * p.slice];
+            w.w[b] = load16(p.w + (size_t)step(b) * (K * kWBytes<ACT>) + 256 * (size_t)s, p.wo);
+            if (ACT == kMXFP8) w.sc[b] = (p.s + (size_t)(2 * s) * rows * 4 + 4 * step(b))[p.so];
         }
+#pragma unroll
+        for (int g = 0; g < NT; ++g)
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                for (int i = 0; i < Seg<ACT>::kX; ++i)
+                    o.x[g][t][i] = load16(x + t * (size_t)term + (size_t)(Seg<ACT>::kXBytes * s + 16 * i), in.x[g]);
     } else {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            o.w[b] = (u32x4){0u, 0u, 0u, 0u};
-            o.sc[b] = 127u;
+            w.w[b] = (u32x4){0u, 0u, 0u, 0u};
+            w.sc[b] = 127u;
         }
+#pragma unroll
+        for (int g = 0; g < NT; ++g)
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                for (int i = 0; i < Seg<ACT>::kX; ++i) o.x[g][t][i] = (u32x4){0u, 0u, 0u, 0u};
     }
-}
-template <int ACT, int NT, int TERMS>
-__device__ __forceinline__ void load(const Acts<ACT, NT, TERMS>& p, int s, int K, ActPiece<ACT, NT, TERMS>& o) {
-    const bool in = inside<ACT>(s, K);
-#pragma unroll
-    for (int g = 0; g < NT; ++g)
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t)
-#pragma unroll
-            for (int i = 0; i < Seg<ACT>::kX; ++i) {
-                if (in) o.x[g][t][i] = *reinterpret_cast<const u32x4*>(p.x[g] + t * p.term + Seg<ACT>::kXBytes * s + 16 * i);
-                else o.x[g][t][i] = (u32x4){0u, 0u, 0u, 0u};
-            }
 }
 
 // Eight E4M3 codes times 2^(byte - 127) as bfloat16 (exact).
@@ -294,44 +296,20 @@ __device__ __forceinline__ void multiply(const WeightPiece<ACT, NB>& w, const Ac
     }
 }
 
-// sum[b][g]: of weight row 4 b + lane / 16 and row 4 g + (lane % 16) / 4, the same on the four lanes of a quad: the
-// product over the segments [s0, s1), D of them requested ahead.
-template <int ACT, int NB, int NT, int TERMS, int D>
-__device__ __forceinline__ void product(const Weights<ACT, NB>& p, const Acts<ACT, NT, TERMS>& in, int s0, int s1,
-                                        float (&sum)[NB][NT]) {
-    WeightPiece<ACT, NB> w[D];
-    ActPiece<ACT, NT, TERMS> x[D];
-    f32x4 acc[NB][NT];
+template <int NB, int NT>
+__device__ __forceinline__ void clear(f32x4 (&acc)[NB][NT]) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int g = 0; g < NT; ++g) acc[b][g] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int u = 0; u < D; ++u)
-        if (s0 + u < s1) {
-            load(p, s0 + u, w[u]);
-            load(in, s0 + u, p.K, x[u]);
-        }
-    for (int s = s0; s < s1; s += D) {
-#pragma unroll
-        for (int u = 0; u < D; ++u) {
-            if (s + u >= s1) break;
-            multiply<ACT, NB, NT, TERMS>(w[u], x[u], acc);
-            if (s + u + D < s1) {
-                load(p, s + u + D, w[u]);
-                load(in, s + u + D, p.K, x[u]);
-            }
-        }
-    }
-    const int b4 = threadIdx.x & 3;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int g = 0; g < NT; ++g) {
-            const f32x4 v = acc[b][g];
-            const float mine = b4 & 2 ? (b4 & 1 ? v[3] : v[2]) : (b4 & 1 ? v[1] : v[0]);
-            sum[b][g] = __uint_as_float(group_reduce<4>(__float_as_uint(mine), AddF32()));
-        }
+}
+
+// The wanted product of an accumulator: of weight row lane / 16 and activation row (lane % 16) / 4, the same on the
+// four lanes of a quad.
+__device__ __forceinline__ float wanted(const f32x4& v) {
+    const int b = threadIdx.x & 3;
+    const float mine = b & 2 ? (b & 1 ? v[3] : v[2]) : (b & 1 ? v[1] : v[0]);
+    return __uint_as_float(group_reduce<4>(__float_as_uint(mine), AddF32()));
 }
 
 // The routed rows of group g, as a workgroup of 256 finds them in idx: with R <= E
@@ -385,9 +363,10 @@ __device__ __forceinline__ void store_h(float a, float b, void* h, size_t row, i
 }  // namespace
 
 // Gate and up projections: workgroup = (group, 2 NB hidden units), NB / 2 groups
-// of 4 gate rows and as many up; its waves take the quarters of K.
+// of 4 gate rows and as many up; its waves take the quarters of K, D segments of
+// it requested ahead.
 template <int ACT, int NB, int NT, int D>
-__global__ __launch_bounds__(256) void few_up_kernel(const void* __restrict__ x, const int32_t* __restrict__ idx,
+__global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__ x, const int32_t* __restrict__ idx,
                                                      const uint8_t* __restrict__ w1, const uint8_t* __restrict__ s1,
                                                      void* __restrict__ h, int R, int E, int k, int d, int H) {
     __shared__ uint16_t s_rows[kRows];
@@ -400,23 +379,33 @@ __global__ __launch_bounds__(256) void few_up_kernel(const void* __restrict__ x,
     if (n == 0) return;
     const int u0 = units * hb, lane = threadIdx.x & 63, wave = wave_index();
     // packed rows of hidden unit u: gate at 64 (u / 32) + u % 32, up 32 further
-    int row0[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) row0[b] = 64 * (u0 / 32) + u0 % 32 + 4 * (b % (NB / 2)) + 32 * (b / (NB / 2));
-    const size_t expert = (size_t)e * 2 * H * d;
-    const Weights<ACT, NB> p = weights_at<ACT, NB>(w1 + expert * (ACT == kF32 ? 4 : (ACT == kBF16 ? 2 : 1)),
-                                                   s1 + expert / 32, row0, 2 * H, d);
+    const Weights<ACT> p = weights_at<ACT>(w1, s1, e, 64 * (u0 / 32) + u0 % 32, 2 * H, d);
+    auto step = [](int b) { return 4 * (b % (NB / 2)) + 32 * (b / (NB / 2)); };
     const int ns = (d + Seg<ACT>::kElems - 1) / Seg<ACT>::kElems, lo = wave * ns / 4, hi = (wave + 1) * ns / 4;
     for (int n0 = 0; n0 < n; n0 += 4 * NT) {
-        const Acts<ACT, NT, 1> in = acts_at<ACT, NT, 1>(x, s_rows, n0, n, k, d);
-        float sum[NB][NT];
-        product<ACT, NB, NT, 1, D>(p, in, lo, hi, sum);
-        if ((lane & 3) == 0) {
+        const Acts<ACT, NT, 1> in = acts_at<ACT, NT, 1>(s_rows, n0, n, k, d);
+        WeightPiece<ACT, NB> w[D];
+        ActPiece<ACT, NT, 1> a[D];
+        f32x4 acc[NB][NT];
+        clear<NB, NT>(acc);
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+        for (int u = 0; u < D; ++u)
+            if (lo + u < hi) load<ACT, NB, NT, 1>(p, x, in, lo + u, 2 * H, d, step, w[u], a[u]);
+        for (int s = lo; s < hi; s += D) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) red[wave][b][t][lane >> 2] = sum[b][t];   // 4 (weight row) + row
+            for (int u = 0; u < D; ++u) {
+                if (s + u >= hi) break;
+                multiply<ACT, NB, NT, 1>(w[u], a[u], acc);
+                if (s + u + D < hi) load<ACT, NB, NT, 1>(p, x, in, s + u + D, 2 * H, d, step, w[u], a[u]);
+            }
         }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float v = wanted(acc[b][t]);
+                if ((lane & 3) == 0) red[wave][b][t][lane >> 2] = v;   // 4 (weight row) + row
+            }
         __syncthreads();
         for (int o = threadIdx.x; o < units * 4 * NT; o += 256) {
             const int u = o % units, r = o / units, at = 4 * (u & 3) + (r & 3);
@@ -432,70 +421,115 @@ __global__ __launch_bounds__(256) void few_up_kernel(const void* __restrict__ x,
 }
 
 // Down projection and combine: workgroup = 4 NB outputs of every token, its
-// sixteen waves a quarter of K of one expert in turn; the quarters of each
-// routed row's outputs meet in LDS.
-template <int ACT, int NB, int NT, int D>
-__global__ __launch_bounds__(1024) void few_down_kernel(const void* __restrict__ h, const int32_t* __restrict__ idx,
-                                                        const float* __restrict__ gate,
-                                                        const uint8_t* __restrict__ w2, const uint8_t* __restrict__ s2,
-                                                        void* __restrict__ y, int T, int E, int k, int d, int H) {
+// waves a quarter of K of one expert (up to 4 NT rows of it) in turn; the
+// quarters of each routed row's outputs meet in LDS.  A quarter is a few segments,
+// so a wave's requests run on over the ends of its experts: they are made by a
+// cursor of their own, D segments ahead of the products.
+template <int ACT, int NB, int NT, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __restrict__ h, const int32_t* __restrict__ idx,
+                                                              const float* __restrict__ gate,
+                                                              const uint8_t* __restrict__ w2,
+                                                              const uint8_t* __restrict__ s2, void* __restrict__ y, int T,
+                                                              int E, int k, int d, int H) {
     constexpr int TERMS = ACT == kF32 ? 1 : 2;
-    constexpr int cols = 4 * NB;
+    constexpr int cols = 4 * NB, threads = 64 * WAVES;
     __shared__ int32_t s_count[kMaxExperts], s_first[kMaxExperts];
-    __shared__ int32_t s_expert[kRows];
+    __shared__ uint32_t s_item[kRows];      // expert, first row in s_rows, rows: up to 4 NT rows of an expert
     __shared__ uint16_t s_rows[kRows];
-    __shared__ int32_t s_groups, s_total;
+    __shared__ int32_t s_items, s_total;
     extern __shared__ float s_part[];   // [4][T k][cols]
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), R = T * k;
     // the experts in use and their rows; their order does not matter to any sum
-    for (int e = tid; e < E; e += 1024) s_count[e] = 0;
-    if (tid == 0) s_groups = s_total = 0;
+    for (int e = tid; e < E; e += threads) s_count[e] = 0;
+    if (tid == 0) s_items = s_total = 0;
     __syncthreads();
-    int mine = -1, slot = 0;
-    if (tid < R) {
-        mine = idx[tid];
-        if (mine < 0 || mine >= E) mine = -1;
-        else slot = atomicAdd(&s_count[mine], 1);
+    constexpr int kMine = (kRows + threads - 1) / threads;
+    int mine[kMine], slot[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = tid + threads * i;
+        mine[i] = r < R ? idx[r] : -1;
+        if (mine[i] < 0 || mine[i] >= E) mine[i] = -1;
+        slot[i] = mine[i] >= 0 ? atomicAdd(&s_count[mine[i]], 1) : -1;
     }
     __syncthreads();
-    if (mine >= 0 && slot == 0) {
-        s_expert[atomicAdd(&s_groups, 1)] = mine;
-        s_first[mine] = atomicAdd(&s_total, s_count[mine]);
-    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if (slot[i] == 0) {
+            const int n = s_count[mine[i]], first = atomicAdd(&s_total, n), items = (n + 4 * NT - 1) / (4 * NT);
+            s_first[mine[i]] = first;
+            const int at = atomicAdd(&s_items, items);
+            for (int j = 0; j < items; ++j)
+                s_item[at + j] = (uint32_t)mine[i] << 16 | (uint32_t)(first + 4 * NT * j) << 6 | (uint32_t)min(4 * NT, n - 4 * NT * j);
+        }
     __syncthreads();
-    if (mine >= 0) s_rows[s_first[mine] + slot] = (uint16_t)tid;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if (slot[i] >= 0) s_rows[s_first[mine[i]] + slot[i]] = (uint16_t)(tid + threads * i);
     __syncthreads();
-    const int c0 = cols * blockIdx.x, groups = uniform(s_groups);
+    const int c0 = cols * blockIdx.x, items = uniform(s_items);
     const int ns = (H + Seg<ACT>::kElems - 1) / Seg<ACT>::kElems, quarter = wave & 3;
     const int lo = quarter * ns / 4, hi = (quarter + 1) * ns / 4;
-    int row0[NB];
+    auto step = [](int b) { return 4 * b; };
+    const int first_item = wave >> 2;
+    if (lo < hi) {
+        // the requests' cursor
+        int gi = first_item, si = lo;
+        Weights<ACT> p{};
+        Acts<ACT, NT, TERMS> in{};
+        auto enter = [&]() {
+            if (gi >= items) return;
+            const uint32_t it = uniform(s_item[gi]);
+            p = weights_at<ACT>(w2, s2, it >> 16, c0, d, H);
+            in = acts_at<ACT, NT, TERMS>(s_rows + ((it >> 6) & 0x3FF), 0, it & 0x3F, 1, H);
+        };
+        WeightPiece<ACT, NB> w[D];
+        ActPiece<ACT, NT, TERMS> a[D];
+        auto request = [&](int u) {
+            if (gi >= items) return;
+            load<ACT, NB, NT, TERMS>(p, h, in, si, d, H, step, w[u], a[u]);
+            if (++si == hi) {
+                si = lo;
+                gi += WAVES / 4;
+                enter();
+            }
+        };
+        enter();
 #pragma unroll
-    for (int b = 0; b < NB; ++b) row0[b] = c0 + 4 * b;
-    for (int g = wave >> 2; g < groups; g += 4) {
-        const int e = uniform(s_expert[g]), n = uniform(s_count[e]);
-        const uint16_t* rows = s_rows + uniform(s_first[e]);
-        const size_t expert = (size_t)e * d * H;
-        const Weights<ACT, NB> p = weights_at<ACT, NB>(w2 + expert * (ACT == kF32 ? 4 : (ACT == kBF16 ? 2 : 1)),
-                                                       s2 + expert / 32, row0, d, H);
-        for (int n0 = 0; n0 < n; n0 += 4 * NT) {
-            const Acts<ACT, NT, TERMS> in = acts_at<ACT, NT, TERMS>(h, rows, n0, n, 1, H);
-            float sum[NB][NT];
-            product<ACT, NB, NT, TERMS, D>(p, in, lo, hi, sum);
-            if ((lane & 3) == 0) {
+        for (int u = 0; u < D; ++u) request(u);
+        f32x4 acc[NB][NT];
+        clear<NB, NT>(acc);
+        for (int g = first_item, s = lo; g < items;) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const int r = n0 + 4 * t + ((lane & 15) >> 2);
-                    if (r < n) {
+            for (int u = 0; u < D; ++u) {
+                if (g >= items) break;
+                multiply<ACT, NB, NT, TERMS>(w[u], a[u], acc);
+                request(u);
+                if (++s == hi) {
+                    const uint32_t it = uniform(s_item[g]);
+                    const uint16_t* rows = s_rows + ((it >> 6) & 0x3FF);
+                    const int n = it & 0x3F;
 #pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            s_part[((size_t)quarter * R + rows[r]) * cols + 4 * b + (lane >> 4)] = sum[b][t];
+                    for (int t = 0; t < NT; ++t) {
+                        const int r = 4 * t + lane_row();
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const float v = wanted(acc[b][t]);
+                            if ((lane & 3) == 0 && r < n)
+                                s_part[((size_t)quarter * R + rows[r]) * cols + 4 * b + (lane >> 4)] = v;
+                        }
                     }
+                    clear<NB, NT>(acc);
+                    s = lo;
+                    g += WAVES / 4;
                 }
             }
         }
+    } else {   // a quarter without a segment
+        for (int o = lane + 64 * first_item; o < R * cols; o += 16 * WAVES) s_part[(size_t)quarter * R * cols + o] = 0.f;
     }
     __syncthreads();
-    for (int o = tid; o < T * cols; o += 1024) {
+    for (int o = tid; o < T * cols; o += threads) {
         const int t = o / cols, c = o % cols;
         float s = 0.f;
         for (int j = 0; j < k; ++j) {
@@ -512,20 +546,47 @@ __global__ __launch_bounds__(1024) void few_down_kernel(const void* __restrict__
 
 namespace {
 
+#ifndef UNB
+#define UNB 4
+#endif
+#ifndef UD
+#define UD 1
+#endif
+#ifndef DNB
+#define DNB 2
+#endif
+#ifndef DD
+#define DD 3
+#endif
+#ifndef DW
+#define DW 8
+#endif
+
+template <int ACT, int NT>
+hipError_t launch_products(const void* x_, const int32_t* idx, const float* gate, const uint8_t* w1, const uint8_t* w2,
+                           const uint8_t* s1, const uint8_t* s2, void* h_, void* y, int T, int d, int E, int k, int H,
+                           hipStream_t s) {
+    const int R = T * k, G = std::min(R, E);
+    const uint8_t *x = static_cast<const uint8_t*>(x_), *h = static_cast<const uint8_t*>(h_);
+    hipLaunchKernelGGL((few_up_kernel<ACT, UNB, NT, UD>), dim3(G * (H / (2 * UNB))), dim3(256), 0, s, x, idx, w1, s1, h_, R, E, k, d, H);
+    // LDS for the quarters of all rows: 32 KB at most
+    if (R <= 512 / DNB)
+        hipLaunchKernelGGL((few_down_kernel<ACT, DNB, NT, DD, DW>), dim3(d / (4 * DNB)), dim3(64 * DW), (size_t)4 * R * 4 * DNB * 4, s, h, idx, gate, w2,
+                           s2, y, T, E, k, d, H);
+    else
+        hipLaunchKernelGGL((few_down_kernel<ACT, 1, NT, DD, DW>), dim3(d / 4), dim3(64 * DW), (size_t)4 * R * 4 * 4, s, h, idx, gate, w2,
+                           s2, y, T, E, k, d, H);
+    return hipGetLastError();
+}
+
 template <int ACT>
 hipError_t launch_products(const void* x, const int32_t* idx, const float* gate, const uint8_t* w1, const uint8_t* w2,
                            const uint8_t* s1, const uint8_t* s2, void* h, void* y, int T, int d, int E, int k, int H,
                            hipStream_t s) {
-    const int R = T * k, G = std::min(R, E);
-    hipLaunchKernelGGL((few_up_kernel<ACT, 4, 4, 1>), dim3(G * (H / 8)), dim3(256), 0, s, x, idx, w1, s1, h, R, E, k, d, H);
-    // LDS for the quarters of all rows: 32 KB at most
-    if (R <= 256)
-        hipLaunchKernelGGL((few_down_kernel<ACT, 2, 4, 1>), dim3(d / 8), dim3(1024), (size_t)4 * R * 8 * 4, s, h, idx, gate, w2,
-                           s2, y, T, E, k, d, H);
-    else
-        hipLaunchKernelGGL((few_down_kernel<ACT, 1, 4, 1>), dim3(d / 4), dim3(1024), (size_t)4 * R * 4 * 4, s, h, idx, gate, w2,
-                           s2, y, T, E, k, d, H);
-    return hipGetLastError();
+    const float rows = (float)T * k / E;   // of an expert, on average
+    if (T <= 4 || rows <= 2.f) return launch_products<ACT, 1>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    if (T <= 8 || rows <= 5.f) return launch_products<ACT, 2>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    return launch_products<ACT, 4>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
 }
 
 }  // namespace

@@ -36,6 +36,7 @@ namespace moe {
 namespace {
 
 constexpr int kRows = kFewTokens * kMaxTopK;
+constexpr int kFewSlice = 2048;   // most rows of W_r a workgroup of the router takes
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int wave_index() { return uniform((int)(threadIdx.x >> 6)); }
@@ -49,71 +50,106 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// A workgroup per token: logits (LEARNED, E / NV a power of two up to 64, NV
-// values a 16-byte load), selection, gates.  Wave w takes the w-th sixteenth of
-// d, its lanes consecutive 16-byte pieces of W_r; an expert's rank is the number
-// of experts before it, counted by 1024 / E threads each.
-template <bool LEARNED, bool BF>
-__global__ __launch_bounds__(1024) void few_route_kernel(const void* __restrict__ x, const void* __restrict__ w,
-                                                         float* __restrict__ logits,
-                                                         const uint8_t* __restrict__ mask, int32_t* __restrict__ idx,
-                                                         float* __restrict__ gate, int E, int k, int d) {
+// Partial logits of a token over a sixteenth of d, a workgroup each: part [T][16][E].
+// W_r's rows are E / NV pieces of 16 bytes (C of them) and lie one after the
+// other, so the workgroup's first 256 / C * C threads read consecutive pieces
+// and keep their column.
+template <bool BF>
+__global__ __launch_bounds__(256) void few_logits_kernel(const u32x4* __restrict__ x, const u32x4* __restrict__ w,
+                                                         float* __restrict__ part, int E, int d) {
     constexpr int NV = BF ? 8 : 4;
+    constexpr int kB = 8;
+    __shared__ float s_x[kFewSlice];
+    __shared__ float red[256 * NV];
+    const int t = blockIdx.y, tid = threadIdx.x, rows = d / kFewSlices, C = E / NV;
+    const int by = 256 / C, n = rows * C;          // rows of a step; pieces of the slice
+    const u32x4* wp = w + (size_t)blockIdx.x * n;
+    const bool on = tid < by * C;
+    u32x4 r[kB];
+    auto request = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < kB; ++u) r[u] = wp[min(p0 + u * by * C + tid, n - 1)];
+    };
+    request(0);
+    for (int c = tid; c < rows / NV + 1; c += 256) {   // d / 16 is a multiple of 4: the last piece may be half another's
+        const size_t first = ((size_t)t * d + (size_t)blockIdx.x * rows) / NV;
+        const int off = (int)(((size_t)t * d + (size_t)blockIdx.x * rows) % NV);
+        if (NV * c - off >= rows) continue;
+        float v[8];
+        unpack16<BF>(x[first + c], v);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (NV * c + i >= off && NV * c + i - off < rows) s_x[NV * c + i - off] = v[i];
+    }
+    __syncthreads();
+    float acc[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+    for (int p0 = 0; p0 < n; p0 += kB * by * C) {
+        if (p0) request(p0);
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+            const int p = p0 + u * by * C + tid;
+            if (!on || p >= n) continue;
+            float v[8];
+            unpack16<BF>(r[u], v);
+            const float xv = s_x[p / C];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) acc[i] = fmaf(xv, v[i], acc[i]);
+        }
+    }
+    // red [by][E]; the rows in order, 256 / E (at least one) ranges of them by a thread each, then the ranges
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) red[NV * tid + i] = acc[i];
+    }
+    __syncthreads();
+    const int ranges = min(by, max(1, 256 / E)), len = (by + ranges - 1) / ranges;
+    for (int e = tid; e < E * ranges; e += 256) {
+        const int g = e / E;
+        float s = 0.f;
+        for (int j = g * len; j < min(by, (g + 1) * len); ++j) s += red[j * E + e % E];
+        acc[0] = s;   // E ranges > 256 only with one range: then the sum is the result
+        if (ranges == 1) part[((size_t)t * kFewSlices + blockIdx.x) * E + e] = s;
+    }
+    if (ranges == 1) return;
+    __syncthreads();
+    if (tid < E * ranges) red[tid] = acc[0];
+    __syncthreads();
+    if (tid < E) {
+        float s = red[tid];
+        for (int g = 1; g < ranges; ++g) s += red[g * E + tid];
+        part[((size_t)t * kFewSlices + blockIdx.x) * E + tid] = s;
+    }
+}
+
+// A workgroup per token: logits from their sixteen parts (NULL: they are given),
+// selection, gates.  An expert's rank is the number of experts before it,
+// counted by 1024 / E threads each.
+__global__ __launch_bounds__(1024) void few_select_kernel(const float* __restrict__ part, float* __restrict__ logits,
+                                                          const uint8_t* __restrict__ mask, int32_t* __restrict__ idx,
+                                                          float* __restrict__ gate, int E, int k) {
     __shared__ float s_logit[kMaxExperts];
     __shared__ int32_t s_rank[kMaxExperts];
     __shared__ float s_val[kMaxTopK];
     __shared__ int32_t s_idx[kMaxTopK];
-    extern __shared__ float s_dyn[];   // x [d], then the waves' sums [16][E]
-    const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-    if (LEARNED) {
-        float* s_x = s_dyn;
-        float* s_sum = s_dyn + d;
-        for (int c = tid; c < d / NV; c += 1024) {
-            float v[8];
-            unpack16<BF>(static_cast<const u32x4*>(x)[(size_t)t * (d / NV) + c], v);
+    const int t = blockIdx.x, tid = threadIdx.x;
+    if (tid < E) {
+        float s;
+        if (part) {
+            const float* p = part + (size_t)t * kFewSlices * E + tid;
+            float v[kFewSlices];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s_x[NV * c + i] = v[i];
-        }
-        __syncthreads();
-        const int C = E / NV;                     // pieces of a row of W_r
-        const int lo = wave * (d / 16), hi = lo + d / 16;
-        const u32x4* wp = static_cast<const u32x4*>(w) + (size_t)lo * C;
-        const int n = (hi - lo) * C, by = 64 / C;  // pieces of this wave's rows; rows of 64 of them
-        float acc[NV];
+            for (int i = 0; i < kFewSlices; ++i) v[i] = p[(size_t)i * E];
+            s = v[0];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) acc[i] = 0.f;
-        constexpr int kB = 8;
-        for (int p = lane; p < n; p += 64 * kB) {
-            u32x4 r[kB];
-#pragma unroll
-            for (int u = 0; u < kB; ++u) r[u] = wp[min(p + 64 * u, n - 1)];
-#pragma unroll
-            for (int u = 0; u < kB; ++u) {
-                if (p + 64 * u >= n) continue;
-                float v[8];
-                unpack16<BF>(r[u], v);
-                const float xv = s_x[lo + p / C + by * u];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) acc[i] = fmaf(xv, v[i], acc[i]);
-            }
-        }
-        for (int m = C; m < 64; m <<= 1)
-#pragma unroll
-            for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor(acc[i], m);
-        if (lane < C) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) s_sum[wave * E + NV * lane + i] = acc[i];
-        }
-        __syncthreads();
-        if (tid < E) {
-            float s = s_sum[tid];
-#pragma unroll
-            for (int v = 1; v < 16; ++v) s += s_sum[v * E + tid];
-            s_logit[tid] = s;
+            for (int i = 1; i < kFewSlices; ++i) s += v[i];
             logits[(size_t)t * E + tid] = s;
+        } else {
+            s = logits[(size_t)t * E + tid];
         }
-    } else if (tid < E) {
-        s_logit[tid] = logits[(size_t)t * E + tid];
+        s_logit[tid] = s;
+        s_rank[tid] = 0;
     }
     if (mask && mask[t] == 0) {
         if (tid < k) {
@@ -122,13 +158,12 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const void* __restrict_
         }
         return;
     }
-    if (tid < E) s_rank[tid] = 0;
     __syncthreads();
-    const int parts = 1024 / E, e = tid % E, part = tid / E;
-    if (part < parts) {
+    const int parts = 1024 / E, e = tid % E, mine_part = tid / E;
+    if (mine_part < parts) {
         const uint32_t mine = logit_key(s_logit[e]);
         int before = 0;
-        for (int o = part; o < E; o += parts) {
+        for (int o = mine_part; o < E; o += parts) {
             const uint32_t other = logit_key(s_logit[o]);
             before += other > mine || (other == mine && o < e);
         }
@@ -592,21 +627,18 @@ hipError_t launch_products(const void* x, const int32_t* idx, const float* gate,
 }  // namespace
 
 bool few_routes_itself(int act, int d, int E) {
-    const int nv = act == kF32 ? 4 : 8, c = E / nv;
-    return E % nv == 0 && c <= 64 && (c & (c - 1)) == 0 && 4 * d + 64 * E <= 48 * 1024;   // its LDS
+    return E % (act == kF32 ? 4 : 8) == 0 && E <= 1024 && d <= kFewSlices * kFewSlice;
 }
 
-hipError_t launch_few(int act, const void* x, const void* w_router, bool learned, float* logits, const uint8_t* mask,
-                      const uint8_t* w1, const uint8_t* w2, const uint8_t* s1, const uint8_t* s2, void* y, int32_t* idx,
-                      float* gate, void* h, int T, int d, int E, int k, int H, hipStream_t s) {
-    const bool bf = act != kF32;
-    const size_t lds = (size_t)(d + 16 * E) * 4;
-    if (!learned)
-        hipLaunchKernelGGL((few_route_kernel<false, true>), dim3(T), dim3(1024), 0, s, x, w_router, logits, mask, idx, gate, E, k, d);
-    else if (bf)
-        hipLaunchKernelGGL((few_route_kernel<true, true>), dim3(T), dim3(1024), lds, s, x, w_router, logits, mask, idx, gate, E, k, d);
-    else
-        hipLaunchKernelGGL((few_route_kernel<true, false>), dim3(T), dim3(1024), lds, s, x, w_router, logits, mask, idx, gate, E, k, d);
+hipError_t launch_few(int act, const void* x, const void* w_router, bool learned, float* logits, float* part,
+                      const uint8_t* mask, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1, const uint8_t* s2,
+                      void* y, int32_t* idx, float* gate, void* h, int T, int d, int E, int k, int H, hipStream_t s) {
+    const u32x4 *xv = static_cast<const u32x4*>(x), *wv = static_cast<const u32x4*>(w_router);
+    if (learned && act != kF32)
+        hipLaunchKernelGGL(few_logits_kernel<true>, dim3(kFewSlices, T), dim3(256), 0, s, xv, wv, part, E, d);
+    else if (learned)
+        hipLaunchKernelGGL(few_logits_kernel<false>, dim3(kFewSlices, T), dim3(256), 0, s, xv, wv, part, E, d);
+    hipLaunchKernelGGL(few_select_kernel, dim3(T), dim3(1024), 0, s, learned ? part : nullptr, logits, mask, idx, gate, E, k);
     const hipError_t st = hipGetLastError();
     if (st != hipSuccess) return st;
     if (act == kF32) return launch_products<kF32>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);

@@ -611,7 +611,7 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  * in float32, per element.
  *
  * moe_param, one tensor of n elements (contiguous, any shape; n = 0 is passed
- * over).  Device pointers, 16-byte aligned:
+ * over).  Device pointers, 16-byte aligned (scales 4):
  *   weight  : [n] w_dtype (MOE_F32 or MOE_BF16), in and out; NULL with master,
  *             m, v and the scales: a gradient for moe_grad_norm only
  *   grad    : [n] g_dtype (MOE_F32 or MOE_BF16)

@@ -305,9 +305,9 @@ int32_t check_param(const moe_param& p) {
     if (p.n == 0) return MOE_OK;   // an empty tensor has no address
     if (!p.grad || (!p.m_scale) != (!p.v_scale)) return MOE_ERR_NULL;
     if (trained ? !p.m || !p.v : p.master || p.m || p.v || p.m_scale) return MOE_ERR_NULL;
-    for (const void* q : {p.weight, (void*)p.grad, (void*)p.master, p.m, p.v, (void*)p.m_scale, (void*)p.v_scale})
+    for (const void* q : {(const void*)p.weight, p.grad, (const void*)p.master, (const void*)p.m, (const void*)p.v})
         if (off_by(q, 16)) return MOE_ERR_ARG;
-    return MOE_OK;
+    return off_by(p.m_scale, 4) || off_by(p.v_scale, 4) ? MOE_ERR_ARG : MOE_OK;
 }
 
 int param_kind(const moe_param& p) {

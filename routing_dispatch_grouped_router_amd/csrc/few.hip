@@ -1,5 +1,6 @@
 // The routed block for a few tokens on the packed weights of moe_pack_weights, for
-// gfx950: three launches, from router logits to y.
+// gfx950: from router logits to y in three launches (four where the selection takes
+// one of its own).
 //
 //   logits = x W_r, top-k and gates;  h[r] = silu(x[t] Wg) (x[t] Wu) for the
 //   routed rows r = t k + j with expert e_r;  y[t] = sum_j g[t][j] h[t k + j] Wd.
@@ -26,6 +27,13 @@
 //
 // Every sum over K is taken in four quarters, added in order, whatever the other
 // rows are: a token's result does not depend on the tokens beside it.
+//
+// The weights' bytes bound it.  d = 4096, E = 64, k = 8, H = 1536, bf16, one token:
+// 62 us (302 MB, 4.9 TB/s; the up projection alone 36 us, 5.6 TB/s, as fast as a
+// kernel that only reads); 16 tokens, d = 2048, E = 8, k = 4, H = 1024: 35 us (101 MB,
+// 2.9 TB/s, of which router and selection 5 us and the launches' starts and ends
+// 6); 7 tokens, two of them padding, of 128 MXFP8 experts, k = 4: 41 us (120 MB).  A
+// 2 GiB copy runs at 4.9 TB/s on the same card.
 #include <algorithm>
 
 #include "moe_device.h"
@@ -36,6 +44,10 @@ namespace moe {
 namespace {
 
 constexpr int kRows = kFewTokens * kMaxTopK;
+// Most logits that the up projection selects from itself.  One token of 64 experts: 62.1 us against 63.9 with a launch
+// of its own, of 128 MXFP8 experts 20.1 and 20.7; 4 tokens of 64 experts 77.7 and 72.8 (4096 workgroups, each of which
+// would select), one of 256 experts 24.6 and 22.6.
+constexpr int kFused = 128;
 constexpr int kFewSlice = 2048;   // most rows of W_r a workgroup of the router takes
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -123,6 +135,25 @@ __global__ __launch_bounds__(256) void few_logits_kernel(const u32x4* __restrict
     }
 }
 
+// The logit of a token and expert from its sixteen parts, in order.
+__device__ __forceinline__ float join_parts(const float* part, int t, int e, int E) {
+    const float* p = part + (size_t)t * kFewSlices * E + e;
+    float v[kFewSlices];
+#pragma unroll
+    for (int i = 0; i < kFewSlices; ++i) v[i] = p[(size_t)i * E];
+    float s = v[0];
+#pragma unroll
+    for (int i = 1; i < kFewSlices; ++i) s += v[i];
+    return s;
+}
+
+// Gate j of the k selected logits, largest first.
+__device__ __forceinline__ float gate_of(const float* val, int k, int j) {
+    float sum = 0.f;
+    for (int i = 0; i < k; ++i) sum += expf(val[i] - val[0]);
+    return expf(val[j] - val[0]) / sum;
+}
+
 // A workgroup per token: logits from their sixteen parts (NULL: they are given),
 // selection, gates.  An expert's rank is the number of experts before it,
 // counted by 1024 / E threads each.
@@ -137,13 +168,7 @@ __global__ __launch_bounds__(1024) void few_select_kernel(const float* __restric
     if (tid < E) {
         float s;
         if (part) {
-            const float* p = part + (size_t)t * kFewSlices * E + tid;
-            float v[kFewSlices];
-#pragma unroll
-            for (int i = 0; i < kFewSlices; ++i) v[i] = p[(size_t)i * E];
-            s = v[0];
-#pragma unroll
-            for (int i = 1; i < kFewSlices; ++i) s += v[i];
+            s = join_parts(part, t, tid, E);
             logits[(size_t)t * E + tid] = s;
         } else {
             s = logits[(size_t)t * E + tid];
@@ -176,10 +201,8 @@ __global__ __launch_bounds__(1024) void few_select_kernel(const float* __restric
     }
     __syncthreads();
     if (tid < k) {
-        float sum = 0.f;
-        for (int j = 0; j < k; ++j) sum += expf(s_val[j] - s_val[0]);
         idx[t * k + tid] = s_idx[tid];
-        gate[t * k + tid] = expf(s_val[tid] - s_val[0]) / sum;
+        gate[t * k + tid] = gate_of(s_val, k, tid);
     }
 }
 
@@ -350,7 +373,8 @@ __device__ __forceinline__ float wanted(const f32x4& v) {
 // The routed rows of group g, as a workgroup of 256 finds them in idx: with R <= E
 // a group per routed row, whose rows are those of its expert if it is the
 // expert's first row (none otherwise), else a group per expert.
-__device__ __forceinline__ int group_rows(const int32_t* idx, int R, int E, int g, int& expert, uint16_t* rows, int32_t* cnt) {
+template <typename Idx>
+__device__ __forceinline__ int group_rows(const Idx& idx, int R, int E, int g, int& expert, uint16_t* rows, int32_t* cnt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
     expert = R <= E ? uniform(idx[g]) : g;
     if (expert < 0 || expert >= E) return 0;
@@ -399,9 +423,13 @@ __device__ __forceinline__ void store_h(float a, float b, void* h, size_t row, i
 
 // Gate and up projections: workgroup = (group, 2 NB hidden units), NB / 2 groups
 // of 4 gate rows and as many up; its waves take the quarters of K, D segments of
-// it requested ahead.
-template <int ACT, int NB, int NT, int D>
-__global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__ x, const int32_t* __restrict__ idx,
+// it requested ahead.  SELECT (T E <= kFused, 256 / (T E) threads for each
+// logit): every workgroup makes the selection for itself, and the first writes
+// it down.
+template <int ACT, int NB, int NT, int D, bool SELECT>
+__global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__ x, int32_t* __restrict__ idx,
+                                                     float* __restrict__ gate, const float* __restrict__ part,
+                                                     float* __restrict__ logits, const uint8_t* __restrict__ mask,
                                                      const uint8_t* __restrict__ w1, const uint8_t* __restrict__ s1,
                                                      void* __restrict__ h, int R, int E, int k, int d, int H) {
     __shared__ uint16_t s_rows[kRows];
@@ -409,8 +437,46 @@ __global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__
     __shared__ float red[4][NB][NT][16];
     constexpr int units = 2 * NB;
     const int nb = H / units, g = blockIdx.x / nb, hb = blockIdx.x - g * nb;
-    int e;
-    const int n = group_rows(idx, R, E, g, e, s_rows, s_cnt);
+    int e, n;
+    if constexpr (SELECT) {
+        __shared__ float s_logit[kFused], s_val[kFused];
+        __shared__ int32_t s_idx[kFused];
+        __shared__ int32_t s_rank[kFused];
+        const int N = R / k * E, tid = threadIdx.x;
+        if (tid < N) {
+            const float v = part ? join_parts(part, tid / E, tid % E, E) : logits[tid];
+            s_logit[tid] = v;
+            s_rank[tid] = 0;
+            if (part && blockIdx.x == 0) logits[tid] = v;
+        }
+        __syncthreads();
+        const int parts = 256 / N, at = tid % N, own = at % E, row = at - own;   // 256 / N threads count for each logit
+        if (tid < parts * N) {
+            const uint32_t key = logit_key(s_logit[at]);
+            int before = 0;
+#pragma unroll 8
+            for (int o = tid / N; o < E; o += parts) {
+                const uint32_t other = logit_key(s_logit[row + o]);
+                before += other > key || (other == key && o < own);
+            }
+            if (parts > 1) atomicAdd(&s_rank[at], before);
+            else s_rank[at] = before;
+        }
+        __syncthreads();
+        if (tid < N && s_rank[tid] < k) {
+            const int t = tid / E;
+            s_idx[t * k + s_rank[tid]] = mask && mask[t] == 0 ? -1 : own;
+            s_val[t * k + s_rank[tid]] = s_logit[tid];
+        }
+        __syncthreads();
+        if (blockIdx.x == 0 && tid < R) {
+            idx[tid] = s_idx[tid];
+            gate[tid] = s_idx[tid] < 0 ? 0.f : gate_of(s_val + tid / k * k, k, tid % k);
+        }
+        n = group_rows(s_idx, R, E, g, e, s_rows, s_cnt);
+    } else {
+        n = group_rows(idx, R, E, g, e, s_rows, s_cnt);
+    }
     if (n == 0) return;
     const int u0 = units * hb, lane = threadIdx.x & 63, wave = wave_index();
     // packed rows of hidden unit u: gate at 64 (u / 32) + u % 32, up 32 further
@@ -474,7 +540,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
     __shared__ int32_t s_items, s_total;
     extern __shared__ float s_part[];   // [4][T k][cols]
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), R = T * k;
-    // the experts in use and their rows; their order does not matter to any sum
+    // the experts in use and their rows, as items of up to 4 NT rows of an expert; their order does not matter to any sum
+    auto item = [](int e, int first, int n) { return (uint32_t)e << 16 | (uint32_t)first << 6 | (uint32_t)n; };
     for (int e = tid; e < E; e += threads) s_count[e] = 0;
     if (tid == 0) s_items = s_total = 0;
     __syncthreads();
@@ -491,18 +558,19 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
         if (slot[i] == 0) {
-            const int n = s_count[mine[i]], first = atomicAdd(&s_total, n), items = (n + 4 * NT - 1) / (4 * NT);
+            const int n = s_count[mine[i]], first = atomicAdd(&s_total, n), m = (n + 4 * NT - 1) / (4 * NT);
             s_first[mine[i]] = first;
-            const int at = atomicAdd(&s_items, items);
-            for (int j = 0; j < items; ++j)
-                s_item[at + j] = (uint32_t)mine[i] << 16 | (uint32_t)(first + 4 * NT * j) << 6 | (uint32_t)min(4 * NT, n - 4 * NT * j);
+            const int at = atomicAdd(&s_items, m);
+            for (int j = 0; j < m; ++j)
+                s_item[at + j] = item(mine[i], first + 4 * NT * j, min(4 * NT, n - 4 * NT * j));
         }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
         if (slot[i] >= 0) s_rows[s_first[mine[i]] + slot[i]] = (uint16_t)(tid + threads * i);
     __syncthreads();
-    const int c0 = cols * blockIdx.x, items = uniform(s_items);
+    const int items = uniform(s_items);
+    const int c0 = cols * blockIdx.x;
     const int ns = (H + Seg<ACT>::kElems - 1) / Seg<ACT>::kElems, quarter = wave & 3;
     const int lo = quarter * ns / 4, hi = (quarter + 1) * ns / 4;
     auto step = [](int b) { return 4 * b; };
@@ -581,47 +649,53 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
 
 namespace {
 
-#ifndef UNB
-#define UNB 4
-#endif
-#ifndef UD
-#define UD 1
-#endif
-#ifndef DNB
-#define DNB 2
-#endif
-#ifndef DD
-#define DD 3
-#endif
-#ifndef DW
-#define DW 8
-#endif
+// What the router left for the products: choices (or, `fused`, what they are made of) and where they go.
+struct Choices {
+    bool fused;
+    const float* part;
+    float* logits;
+    const uint8_t* mask;
+    int32_t* idx;
+    float* gate;
+};
 
 template <int ACT, int NT>
-hipError_t launch_products(const void* x_, const int32_t* idx, const float* gate, const uint8_t* w1, const uint8_t* w2,
-                           const uint8_t* s1, const uint8_t* s2, void* h_, void* y, int T, int d, int E, int k, int H,
-                           hipStream_t s) {
+hipError_t launch_products(const void* x_, const Choices& c, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1,
+                           const uint8_t* s2, void* h_, void* y, int T, int d, int E, int k, int H, hipStream_t s) {
     const int R = T * k, G = std::min(R, E);
     const uint8_t *x = static_cast<const uint8_t*>(x_), *h = static_cast<const uint8_t*>(h_);
-    hipLaunchKernelGGL((few_up_kernel<ACT, UNB, NT, UD>), dim3(G * (H / (2 * UNB))), dim3(256), 0, s, x, idx, w1, s1, h_, R, E, k, d, H);
-    // LDS for the quarters of all rows: 32 KB at most
-    if (R <= 512 / DNB)
-        hipLaunchKernelGGL((few_down_kernel<ACT, DNB, NT, DD, DW>), dim3(d / (4 * DNB)), dim3(64 * DW), (size_t)4 * R * 4 * DNB * 4, s, h, idx, gate, w2,
-                           s2, y, T, E, k, d, H);
+    const dim3 up(G * (H / 8));
+    if (c.fused)
+        hipLaunchKernelGGL((few_up_kernel<ACT, 4, NT, 1, true>), up, dim3(256), 0, s, x, c.idx, c.gate, c.part, c.logits,
+                           c.mask, w1, s1, h_, R, E, k, d, H);
     else
-        hipLaunchKernelGGL((few_down_kernel<ACT, 1, NT, DD, DW>), dim3(d / 4), dim3(64 * DW), (size_t)4 * R * 4 * 4, s, h, idx, gate, w2,
-                           s2, y, T, E, k, d, H);
+        hipLaunchKernelGGL((few_up_kernel<ACT, 4, NT, 1, false>), up, dim3(256), 0, s, x, c.idx, nullptr, nullptr, nullptr,
+                           nullptr, w1, s1, h_, R, E, k, d, H);
+    constexpr int D = NT == 1 ? 3 : 2;
+    // LDS for the quarters of all rows: 32 KB at most
+    if (R <= 256)
+        hipLaunchKernelGGL((few_down_kernel<ACT, 2, NT, D, 8>), dim3(d / 8), dim3(512), (size_t)R * 128, s, h, c.idx,
+                           c.gate, w2, s2, y, T, E, k, d, H);
+    else
+        hipLaunchKernelGGL((few_down_kernel<ACT, 1, NT, D, 8>), dim3(d / 4), dim3(512), (size_t)R * 64, s, h, c.idx,
+                           c.gate, w2, s2, y, T, E, k, d, H);
     return hipGetLastError();
 }
 
+// Activation rows that a reading of the weights serves: 4 NT.  More of them cost
+// loads and registers whether an expert has them or not (bf16, 16 tokens, d =
+// 2048, E = 8, k = 4, 8 rows an expert on average: 36 us with 8 rows, 38 with 16; 32 tokens,
+// 16 rows: 51 and 48).  Float32 and MXFP8 weights take 8 at most: a second
+// reading comes from the caches and costs less than the registers (MXFP8, 16
+// rows an expert: 39 us with 8, 40 with 16; float32 77 and 84).
 template <int ACT>
-hipError_t launch_products(const void* x, const int32_t* idx, const float* gate, const uint8_t* w1, const uint8_t* w2,
-                           const uint8_t* s1, const uint8_t* s2, void* h, void* y, int T, int d, int E, int k, int H,
-                           hipStream_t s) {
+hipError_t launch_products(const void* x, const Choices& c, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1,
+                           const uint8_t* s2, void* h, void* y, int T, int d, int E, int k, int H, hipStream_t s) {
     const float rows = (float)T * k / E;   // of an expert, on average
-    if (T <= 4 || rows <= 2.f) return launch_products<ACT, 1>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
-    if (T <= 8 || rows <= 5.f) return launch_products<ACT, 2>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
-    return launch_products<ACT, 4>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    if (T <= 4 || rows <= 2.f) return launch_products<ACT, 1>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    if constexpr (ACT == kBF16)
+        if (T > 8 && rows > 9.f) return launch_products<ACT, 4>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    return launch_products<ACT, 2>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
 }
 
 }  // namespace
@@ -638,12 +712,14 @@ hipError_t launch_few(int act, const void* x, const void* w_router, bool learned
         hipLaunchKernelGGL(few_logits_kernel<true>, dim3(kFewSlices, T), dim3(256), 0, s, xv, wv, part, E, d);
     else if (learned)
         hipLaunchKernelGGL(few_logits_kernel<false>, dim3(kFewSlices, T), dim3(256), 0, s, xv, wv, part, E, d);
-    hipLaunchKernelGGL(few_select_kernel, dim3(T), dim3(1024), 0, s, learned ? part : nullptr, logits, mask, idx, gate, E, k);
+    const Choices c{T * E <= kFused, learned ? part : nullptr, logits, mask, idx, gate};
+    if (!c.fused)
+        hipLaunchKernelGGL(few_select_kernel, dim3(T), dim3(1024), 0, s, c.part, logits, mask, idx, gate, E, k);
     const hipError_t st = hipGetLastError();
     if (st != hipSuccess) return st;
-    if (act == kF32) return launch_products<kF32>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
-    if (act == kBF16) return launch_products<kBF16>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
-    return launch_products<kMXFP8>(x, idx, gate, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    if (act == kF32) return launch_products<kF32>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    if (act == kBF16) return launch_products<kBF16>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    return launch_products<kMXFP8>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
 }
 
 }  // namespace moe

@@ -117,7 +117,8 @@ def test_param_table():
         assert _table(_param(**kw))[0] == want, kw
     for name in ("weight", "grad", "m", "v"):
         assert _table(_param(**{name: 0x70004}))[0] == -7
-    assert _table(_param(m_scale=0x50004, v_scale=0x60000))[0] == -7
+    assert _table(_param(m_scale=0x50002, v_scale=0x60000))[0] == -7
+    assert _table(_param(m_scale=0x50004, v_scale=0x60000))[0] == 0
     # tensors that a step writes and others: 100 float32 are 400 bytes
     for name in ("grad", "m", "v"):
         assert _table(_param(**{name: 0x10000 + 384}))[0] == -7

@@ -652,7 +652,8 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  *   norm_clip : device float32 [2] out
  *
  * moe_adamw: one step of every tensor.
- *   hyper : host; betas in [0, 1), eps >= 0, seed of the random bits
+ *   hyper : host; betas in [0, 1), eps >= 0 (0: an element whose gradients were
+ *           all 0 becomes NaN), seed of the random bits
  *   lr    : device float32 [1]
  *   clip  : device float32 [2] as moe_grad_norm writes it, or NULL.  If the
  *           factor is infinite or NaN the step is left out: nothing changes

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -755,23 +756,21 @@ class _Params:
         self._index = self.grads[0].get_device()
         self.norm = torch.empty((2,), dtype=torch.float32, device=self._device)
         n = len(self.grads)
-        fields = dict(grad=self.grads, weight=weights, **more)
         params = (Param * n)()
-        for i, p in enumerate(params):
-            p.n, p.g_dtype = self.grads[i].numel(), _param_type(self.grads[i], "grads")
-            if weights is not None:
-                if weights[i].shape != self.grads[i].shape:
-                    raise ValueError(f"grads: expected {tuple(weights[i].shape)}, got {tuple(self.grads[i].shape)}")
-                p.w_dtype = _param_type(weights[i], "weights")
-            for name, values in fields.items():
-                if values is None:
-                    continue
-                value = values[i]
-                if isinstance(value, torch.Tensor):
-                    if value.device != self._device:
-                        raise ValueError(f"{name} is on {value.device}, expected {self._device}")
-                    value = _ptr(value)
-                setattr(p, name, value)
+        table = np.frombuffer(params, dtype=np.dtype(Param))   # column by column: a tenth of the time of one by one
+        table["n"] = [g.numel() for g in self.grads]
+        table["g_dtype"] = [_param_type(g, "grads") for g in self.grads]
+        table["grad"] = _addresses("grads", self.grads, self._index)
+        if weights is not None:
+            for w, g in zip(weights, self.grads):
+                if w.shape != g.shape:
+                    raise ValueError(f"grads: expected {tuple(w.shape)}, got {tuple(g.shape)}")
+            table["w_dtype"] = [_param_type(w, "weights") for w in weights]
+            table["weight"] = _addresses("weights", weights, self._index)
+        for name, values in more.items():
+            if values is not None:
+                numbers = name in ("weight_decay", "lr_scale")
+                table[name] = values if numbers else _addresses(name, values, self._index)
         size, self._plan = _SZ(), ParamPlan()
         _check("moe_param_table_bytes", lib().moe_param_table_bytes(params, n, ctypes.byref(size)))
         host = torch.empty(size.value, dtype=torch.uint8)
@@ -779,7 +778,13 @@ class _Params:
                                                         ctypes.byref(self._plan)))
         self._table = host.to(self._device)
         torch.cuda.current_stream(self._device).synchronize()   # the calls may run on other streams
-        self._plan_p, self._table_p, self._norm_p = ctypes.byref(self._plan), _own(self._table), _own(self.norm)
+        self._plan_p, self._table_p = ctypes.byref(self._plan), _own(self._table)
+        self._norm_p = _own(self.norm)   # the last of them: nothing is replaced from here on
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__ and "_norm_p" in self.__dict__:
+            raise AttributeError(f"{name}: the tensors stay where they are; write into them, or make another object")
+        object.__setattr__(self, name, value)
 
     def _on_device(self):
         if torch.cuda.current_device() != self._index:
@@ -792,6 +797,23 @@ class _Params:
         _check("moe_grad_norm", lib().moe_grad_norm(self._plan_p, self._table_p, max_norm, self._norm_p,
                                                     _stream(stream, self._index)))
         return self.norm
+
+
+def _addresses(name, tensors, index):
+    """Addresses of tensors (0 for None), contiguous and on one device."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(0)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a device tensor")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        out.append(t.data_ptr())
+    return out
 
 
 def _param_type(t, name):
@@ -838,8 +860,8 @@ class AdamW(_Params):
         def many(name, given, dtype, count):
             """A list of tensors like the weights', `given` or zero."""
             if given is None:
-                return [torch.zeros((count(w.numel()),) if count else w.shape, dtype=dtype, device=device) for w in weights]
-            given = list(given)
+                return tuple(torch.zeros((count(w.numel()),) if count else w.shape, dtype=dtype, device=device) for w in weights)
+            given = tuple(given)
             if len(given) != len(weights):
                 raise ValueError(f"{name}: expected {len(weights)} tensors, got {len(given)}")
             for t, w in zip(given, weights):
@@ -850,16 +872,14 @@ class AdamW(_Params):
             return (n + 127) // 128
         moment = torch.uint8 if eight else torch.float32
         self.m = many("m", m, moment, None)
-        self.m_scale = self.r_scale = self.v = self.r = None
-        if eight:
-            self.r = many("r", r, moment, None)
-            self.m_scale, self.r_scale = many("m_scale", m_scale, torch.float32, blocks), many("r_scale", r_scale, torch.float32, blocks)
-        else:
-            self.v = many("v", v, moment, None)
+        self.v = None if eight else many("v", v, moment, None)
+        self.r = many("r", r, moment, None) if eight else None
+        self.m_scale = many("m_scale", m_scale, torch.float32, blocks) if eight else None
+        self.r_scale = many("r_scale", r_scale, torch.float32, blocks) if eight else None
         if master is True:
             master = [w.float() if w.dtype == torch.bfloat16 else None for w in weights]
         if master is not None:
-            master = list(master)
+            master = tuple(master)
             if len(master) != len(weights):
                 raise ValueError(f"master: expected {len(weights)}, got {len(master)}")
             for t, w in zip(master, weights):

@@ -372,6 +372,12 @@ def test_refusals():
         B.AdamW([w], [g[:5]])
     with pytest.raises(ValueError, match="device tensor"):
         B.AdamW([w], [g.cpu()])
+    op = B.AdamW([w], [g])
+    for name in ("m", "v", "weights", "grads", "lr", "norm", "step", "states"):
+        with pytest.raises(AttributeError):
+            setattr(op, name, None)
+    with pytest.raises(TypeError):
+        op.m[0] = w
     op = B.AdamW([w], [g], betas=(1.0, 0.9))
     with pytest.raises(B.MoeError, match="status -7"):
         op()

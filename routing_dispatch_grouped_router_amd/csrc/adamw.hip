@@ -307,6 +307,9 @@ template <int W, bool S8, typename G, bool NT>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
     const ParamDesc* descs = reinterpret_cast<const ParamDesc*>(a.table + a.descs);
     const uint32_t* map = reinterpret_cast<const uint32_t*>(a.table + a.map);
+    Tensor tensor;
+    int c = a.first + blockIdx.x;
+    if (c < a.end) tensor.at(descs, map, c);   // requested before what the step needs is worked out
     const int32_t taken = *reinterpret_cast<const volatile int32_t*>(a.step);
     const float factor = a.clip ? a.clip[1] : 1.f;
     const bool finite = fabsf(factor) < INFINITY;
@@ -323,13 +326,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
         s.g2 = (float)(1.0 - a.beta2);
         s.eps = a.eps;
         s.key = mix(mix(t) ^ a.seed);
-        Tensor t_;
-        uint32_t key = 0u;
-        for (int c = a.first + blockIdx.x; c < a.end; c += gridDim.x) {
-            if (t_.at(descs, map, c)) key = mix(s.key + t_.d.index);
-            const uint64_t base = t_.base(c);
-            if (base + kParamChunk <= t_.d.n) adamw_chunk<W, S8, G, NT, true>(t_.d, base, s, key);
-            else adamw_chunk<W, S8, G, NT, false>(t_.d, base, s, key);
+        uint32_t key = mix(s.key + tensor.d.index);
+        for (; c < a.end; c += gridDim.x) {
+            if (tensor.at(descs, map, c)) key = mix(s.key + tensor.d.index);
+            const uint64_t base = tensor.base(c);
+            if (base + kParamChunk <= tensor.d.n) adamw_chunk<W, S8, G, NT, true>(tensor.d, base, s, key);
+            else adamw_chunk<W, S8, G, NT, false>(tensor.d, base, s, key);
         }
     }
     if (!a.count) return;

@@ -8,9 +8,8 @@
 //
 // One launch for all tensors of a kind: a table in device memory says where they
 // are, a workgroup takes chunks of 2048 elements, eight consecutive ones a
-// thread, so that every stream moves in 16-byte pieces.  Elements past a
-// tensor's last multiple of eight go one by one; nothing outside a tensor is
-// touched.
+// thread, so that every stream moves in 16-byte pieces.  The wave that holds a
+// tensor's end goes element by element; nothing outside a tensor is touched.
 //
 // Moments in 8 bits: m and r = sqrt(v) as E4M3 codes times a float32 scale,
 // amax / 448, for each 128 elements (the root halves the range that the codes
@@ -30,8 +29,8 @@
 // HBM bounds it: an element's 30 bytes (bf16 weight, float32 master, moments and
 // gradient), 28 (float32) or 12 (bf16 alone, 8-bit moments) are read and
 // written once.  50 M elements (three 8 x 2048 x 1024 tensors and small ones):
-// norm 38 us, 5.2 TB/s; step of bf16 with masters 295 us, 5.1 TB/s; with 8-bit
-// moments and no master 132 us, 4.6 TB/s (a 2 GiB copy runs at 4.9 TB/s on the
+// norm 38 us, 5.2 TB/s; step of bf16 with masters 287 us, 5.3 TB/s; with 8-bit
+// moments and no master 131 us, 4.6 TB/s (a 2 GiB copy runs at 4.9 TB/s on the
 // same card).
 #include <algorithm>
 
@@ -44,6 +43,8 @@ namespace moe {
 namespace {
 
 // ----------------------------------------------------------------------------- eight elements of a stream
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // The tensors' addresses come from memory: said to be global here, so that they
 // are not accessed as what might be LDS too.
@@ -65,7 +66,7 @@ __device__ __forceinline__ void put(void* p, T v) {
 // Elements [i, i + 8) of p as float32; unless FULL those below n, and zero from n on.
 template <bool NT, bool FULL>
 __device__ __forceinline__ void load8(const float* p, uint64_t i, uint64_t n, float (&v)[8]) {
-    if (FULL || i + 8 <= n) {
+    if (FULL) {
         const u32x4 a = get<u32x4, NT>(p + i), b = get<u32x4, NT>(p + i + 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -79,7 +80,7 @@ __device__ __forceinline__ void load8(const float* p, uint64_t i, uint64_t n, fl
 }
 template <bool NT, bool FULL>
 __device__ __forceinline__ void load8(const uint16_t* p, uint64_t i, uint64_t n, float (&v)[8]) {
-    if (FULL || i + 8 <= n) {
+    if (FULL) {
         unpack16<true>(get<u32x4, NT>(p + i), v);
     } else {
 #pragma unroll
@@ -88,7 +89,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, uint64_t i, uint64_t n,
 }
 template <bool NT, bool FULL>
 __device__ __forceinline__ void store8(float* p, uint64_t i, uint64_t n, const float (&v)[8]) {
-    if (FULL || i + 8 <= n) {
+    if (FULL) {
         u32x4 a, b;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -105,7 +106,7 @@ __device__ __forceinline__ void store8(float* p, uint64_t i, uint64_t n, const f
 }
 template <bool NT, bool FULL>
 __device__ __forceinline__ void store8(uint16_t* p, uint64_t i, uint64_t n, const float (&v)[8]) {
-    if (FULL || i + 8 <= n) {
+    if (FULL) {
         put<u32x4, NT>(p + i, pack16<true>(v));
     } else {
 #pragma unroll
@@ -131,7 +132,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 template <bool NT, bool FULL>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, uint64_t i, uint64_t n) {
     u32x2 w = {0u, 0u};
-    if (FULL || i + 8 <= n) {
+    if (FULL) {
         w = get<u32x2, NT>(p + i);
     } else {
 #pragma unroll
@@ -189,7 +190,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scales, uint64_t 
         for (int k = 0; k < 8; ++k)
             if (!(fabsf(v[k]) < INFINITY)) w[k / 4] |= 0x7Fu << (8 * (k % 4));
     }
-    if (FULL || i + 8 <= n) {
+    if (FULL) {
         put<u32x2, NT>(p + i, w);
     } else {
 #pragma unroll
@@ -330,8 +331,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
         for (; c < a.end; c += gridDim.x) {
             if (tensor.at(descs, map, c)) key = mix(s.key + tensor.d.index);
             const uint64_t base = tensor.base(c);
-            if (base + kParamChunk <= tensor.d.n) adamw_chunk<W, S8, G, NT, true>(tensor.d, base, s, key);
-            else adamw_chunk<W, S8, G, NT, false>(tensor.d, base, s, key);
+            if (!S8) __syncthreads();   // waves side by side in each stream: 293 us instead of 302 (below)
+            // the last chunk of a tensor: whole waves as in the others, element by element where its end is
+            if (base + kParamChunk <= tensor.d.n || base + 512 * (uniform(threadIdx.x >> 6) + 1) <= tensor.d.n)
+                adamw_chunk<W, S8, G, NT, true>(tensor.d, base, s, key);
+            else
+                adamw_chunk<W, S8, G, NT, false>(tensor.d, base, s, key);
         }
     }
     if (!a.count) return;
@@ -359,7 +364,9 @@ __device__ __forceinline__ double squares(const G* p, uint64_t e0, uint64_t e1, 
 #pragma unroll
         for (int u = 0; u < kB; ++u) {
             const uint64_t c = e + u * by;
-            if (c < e1) load8<NT, false>(p, c + 8 * threadIdx.x, n, g[u]);
+            if (c >= e1) continue;
+            if (c + 512 * (uniform(threadIdx.x >> 6) + 1) <= n) load8<NT, true>(p, c + 8 * threadIdx.x, n, g[u]);
+            else load8<NT, false>(p, c + 8 * threadIdx.x, n, g[u]);
         }
 #pragma unroll
         for (int u = 0; u < kB; ++u)
@@ -410,15 +417,17 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(unsigned char* table, si
     }
 }
 
-// Workgroups.  32-bit moments: 512, through the caches: six to eight streams keep
-// DRAM at 5.1 TB/s from two waves a SIMD, and more of them at once only scatter
-// its accesses (50 M elements, bf16 with master: 295 us; 1024 workgroups 306,
-// 2048 316, past the caches 315 to 340, 384 and 640 workgroups 340).  8-bit moments:
-// 2048, past the caches: the arithmetic (300 cycles an element of a wave's 64)
-// needs the waves (132 us; 1024 workgroups 134, 512 161, through the caches 137).
+// Workgroups.  32-bit moments: one or two a compute unit, through the caches:
+// six to eight streams are DRAM's to keep apart, and more of them at once scatter
+// its accesses (50 M elements, bf16 with master: 256 workgroups 287 us, 5.3 TB/s;
+// 512 293, 1024 and 2048 300, past the caches 295 to 345, 384 and 640 workgroups
+// 340; 0.8 M elements: 256 9.3 us, 512 8.4).  8-bit moments: 2048, past the caches:
+// the arithmetic (300 cycles an element of a wave's 64) needs the waves (131 us;
+// 1024 workgroups 134, 512 161, through the caches 137).
 template <int W, bool S8, typename G>
 void launch_kind(const AdamArgs& a, hipStream_t s) {
-    const dim3 g(std::max(1, std::min(a.end - a.first, S8 ? 2048 : 512))), b(256);
+    const int chunks = a.end - a.first, most = S8 ? 2048 : (chunks >= 8192 ? 256 : 512);
+    const dim3 g(std::max(1, std::min(chunks, most))), b(256);
     if (S8 && a.nt) hipLaunchKernelGGL((adamw_kernel<W, S8, G, S8>), g, b, 0, s, a);
     else hipLaunchKernelGGL((adamw_kernel<W, S8, G, false>), g, b, 0, s, a);
 }

@@ -537,6 +537,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
     __shared__ int32_t s_count[kMaxExperts], s_first[kMaxExperts];
     __shared__ uint32_t s_item[kRows];      // expert, first row in s_rows, rows: up to 4 NT rows of an expert
     __shared__ uint16_t s_rows[kRows];
+    __shared__ float s_gate[kRows];
+    __shared__ uint8_t s_used[kRows];       // whether a slot is in use
     __shared__ int32_t s_items, s_total;
     extern __shared__ float s_part[];   // [4][T k][cols]
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), R = T * k;
@@ -552,6 +554,10 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
         const int r = tid + threads * i;
         mine[i] = r < R ? idx[r] : -1;
         if (mine[i] < 0 || mine[i] >= E) mine[i] = -1;
+        if (r < R) {
+            s_gate[r] = gate[r];
+            s_used[r] = mine[i] >= 0;
+        }
         slot[i] = mine[i] >= 0 ? atomicAdd(&s_count[mine[i]], 1) : -1;
     }
     __syncthreads();
@@ -634,13 +640,13 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
     __syncthreads();
     for (int o = tid; o < T * cols; o += threads) {
         const int t = o / cols, c = o % cols;
+        const float* q = s_part + (size_t)t * k * cols + c;
+        const int by = R * cols;
         float s = 0.f;
-        for (int j = 0; j < k; ++j) {
-            const int r = t * k + j, e = idx[r];
-            if (e < 0 || e >= E) continue;
-            const float* q = s_part + (size_t)r * cols + c;
-            const size_t by = (size_t)R * cols;
-            s = fmaf(gate[r], ((q[0] + q[by]) + q[2 * by]) + q[3 * by], s);
+#pragma unroll 4
+        for (int j = 0; j < k; ++j, q += cols) {
+            const float v = ((q[0] + q[by]) + q[2 * by]) + q[3 * by];   // of a slot not in use, what LDS held
+            s = s_used[t * k + j] ? fmaf(s_gate[t * k + j], v, s) : s;
         }
         if (ACT == kF32) static_cast<float*>(y)[(size_t)t * d + c0 + c] = s;
         else static_cast<uint16_t*>(y)[(size_t)t * d + c0 + c] = f32_to_bf16(s);

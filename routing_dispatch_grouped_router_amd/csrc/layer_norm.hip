@@ -213,10 +213,10 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
 // registers, the next row requested before a row is summed; the workgroup's
 // groups are added in order into one partial row.
 template <bool BF, int TPR, int CH, bool NT>
-__global__ __launch_bounds__(256) void layer_norm_bwd_kernel(LayerNormBwdArgs a) {
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void layer_norm_bwd_kernel(LayerNormBwdArgs a) {
     constexpr int NV = BF ? 8 : 4;
-    constexpr int NG = 256 / TPR;
-    __shared__ float2 red[2][4];
+    constexpr int NG = TPR > 256 ? 1 : 256 / TPR;
+    __shared__ float2 red[2][TPR > 256 ? TPR / 64 : 4];
     extern __shared__ float acc_s[];   // NG > 1: [NG - 1][2][chunks][NV]
     const int lt = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     float wv[CH][8], dw[CH][8], db[CH][8];
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_small_kernel(LayerNormBwd
 // How a backward of T rows of `chunks` 16-byte chunks runs.
 struct LayerNormBwdPlan {
     bool small;   // one launch; the rest describes the other kernels
-    int tpr;      // threads per row: 64, 256, or 0 for the kernels of long rows
+    int tpr;      // threads per row: 64, 256, 512, or 0 for the kernels of long rows
     int ch;       // chunks per thread
     int rows;     // rows per group
     int blocks;   // partial rows
@@ -553,6 +553,9 @@ LayerNormBwdPlan layer_norm_bwd_plan(int T, int chunks) {
     } else if (chunks <= 256 * 4) {
         p.tpr = 256;
         p.ch = chunks <= 256 ? 1 : (chunks <= 512 ? 2 : 4);
+    } else if (chunks <= 512 * 4) {   // (T = 4096, d = 8192, float32 with dsum: 101 us, by the kernels of long rows 184)
+        p.tpr = 512;
+        p.ch = 4;
     }
     const int groups = p.tpr == 64 ? kPartials * 4 : (p.ch > 1 ? kPartials / 2 : kPartials);
     p.rows = (T + groups - 1) / groups;
@@ -578,6 +581,8 @@ void launch_bwd_rows(const LayerNormBwdArgs& a, const LayerNormBwdPlan& p, hipSt
     if (p.tpr == 64) {
         if (p.ch == 1) hipLaunchKernelGGL((layer_norm_bwd_kernel<BF, 64, 1, NT>), g, b, lds, s, a);
         else hipLaunchKernelGGL((layer_norm_bwd_kernel<BF, 64, 2, NT>), g, b, lds, s, a);
+    } else if (p.tpr == 512) {
+        hipLaunchKernelGGL((layer_norm_bwd_kernel<BF, 512, 4, NT>), g, dim3(512), 0, s, a);
     } else {
         if (p.ch == 1) hipLaunchKernelGGL((layer_norm_bwd_kernel<BF, 256, 1, NT>), g, b, 0, s, a);
         else if (p.ch == 2) hipLaunchKernelGGL((layer_norm_bwd_kernel<BF, 256, 2, NT>), g, b, 0, s, a);

@@ -147,7 +147,7 @@ def test_rows_with_nonfinite_values_leave_the_others():
 
 
 BWD_SHAPES = [(1, 64), (1, 4096), (3, 192), (130, 576), (1000, 256), (777, 192), (2100, 1024), (5000, 128),
-              (600, 4096), (70, 8192), (9, 16448), (700, 9216), (4200, 4096)]
+              (600, 4096), (70, 8192), (9, 16448), (700, 9216), (4200, 4096), (5, 32832), (300, 6144)]
 
 
 @pytest.mark.parametrize("dsum", [False, True])
@@ -185,8 +185,8 @@ def test_layer_norm_backward(T, d, act, dsum):
     assert h["dbias"] is None and torch.equal(h["ds"], first["ds"]) and torch.equal(h["dweight"], first["dweight"])
 
 
-# a wave's rows, a workgroup's rows past the caches, rows read twice
-@pytest.mark.parametrize("T, d", [(500, 256), (4200, 4096), (40, 8448)])
+# a wave's rows, a workgroup's rows past the caches, wider ones, rows read twice
+@pytest.mark.parametrize("T, d", [(500, 256), (4200, 4096), (40, 8448), (7, 16448)])
 def test_layer_norm_backward_in_place(T, d):
     rng = np.random.default_rng(5)
     s, dy, e, w = (_rand(rng, sh, "bf16").to(DEV) for sh in ((T, d), (T, d), (T, d), (d,)))

@@ -847,9 +847,9 @@ class AdamW(_Params):
     def __init__(self, weights, grads, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, lr_scale=1.0,
                  master=None, states: str = "f32", seed: int = 0, step=None, m=None, v=None, r=None, m_scale=None,
                  r_scale=None):
-        weights = tuple(weights)
-        if len(weights) != len(tuple(grads)) or not weights:
-            raise ValueError(f"expected as many grads as weights, got {len(tuple(grads))} and {len(weights)}")
+        weights, grads = tuple(weights), tuple(grads)
+        if len(weights) != len(grads) or not weights:
+            raise ValueError(f"expected as many grads as weights, got {len(grads)} and {len(weights)}")
         if states not in ("f32", "8bit"):
             raise ValueError(f"states: expected 'f32' or '8bit', got {states!r}")
         device, eight = weights[0].device, states == "8bit"

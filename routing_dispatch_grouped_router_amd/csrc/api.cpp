@@ -1259,7 +1259,8 @@ int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper
     if (!beta(hyper->beta1) || !beta(hyper->beta2) || !(hyper->eps >= 0.f) || !std::isfinite(hyper->eps) ||
         off_by(table, 16) || off_by(lr, 4) || off_by(clip, 4) || off_by(step, 4))
         return MOE_ERR_ARG;
-    AdamArgs a{static_cast<unsigned char*>(table), plan->descs, plan->map, 0, 0, lr, clip, step, past_caches((size_t)plan->first[kKinds] * kParamChunk * 4), 0, hyper->seed,
+    const bool nt = past_caches((size_t)plan->first[kKinds] * kParamChunk * 4);
+    AdamArgs a{static_cast<unsigned char*>(table), plan->descs, plan->map, 0, 0, lr, clip, step, nt, 0, hyper->seed,
                hyper->beta1, hyper->beta2, hyper->eps};
     int last = 0;   // the last kind with tensors counts the step
     for (int kind = 0; kind < kKinds; ++kind)

@@ -29,9 +29,9 @@
 // rows are: a token's result does not depend on the tokens beside it.
 //
 // The weights' bytes bound it.  d = 4096, E = 64, k = 8, H = 1536, bf16, one token:
-// 62 us (302 MB, 4.9 TB/s; the up projection alone 36 us, 5.6 TB/s, as fast as a
-// kernel that only reads); 16 tokens, d = 2048, E = 8, k = 4, H = 1024: 35 us (101 MB,
-// 2.9 TB/s, of which router and selection 5 us and the launches' starts and ends
+// 61 us (302 MB, 4.9 TB/s; the up projection alone 36 us, 5.6 TB/s, as fast as a
+// kernel that only reads); 16 tokens, d = 2048, E = 8, k = 4, H = 1024: 34 us (101 MB,
+// 3.0 TB/s, of which router and selection 5 us and the launches' starts and ends
 // 6); 7 tokens, two of them padding, of 128 MXFP8 experts, k = 4: 41 us (120 MB).  A
 // 2 GiB copy runs at 4.9 TB/s on the same card.
 #include <algorithm>

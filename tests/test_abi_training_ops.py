@@ -166,6 +166,9 @@ def test_adamw_binding():
                             (([w], [w]), dict(lr=torch.zeros(2)), "lr"), (([w], [w]), dict(step=torch.zeros(2)), "step")):
         with pytest.raises(ValueError, match=match):
             B.AdamW(*args, **kw)
+    # iterators are read once: the only objection left is that the tensors are the host's
+    with pytest.raises(ValueError, match="device tensor"):
+        B.AdamW(iter([w]), iter([w]))
     with pytest.raises(ValueError, match="at least one"):
         B.GradNorm([])
     with pytest.raises(ValueError, match="device tensor"):

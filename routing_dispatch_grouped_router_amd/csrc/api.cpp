@@ -253,7 +253,7 @@ int32_t check_few(const moe_problem* p) {
 static_assert(kFewTokens == MOE_FEW_MAX_TOKENS, "the header's limit");
 
 struct FewLayout {
-    size_t h, idx, gate, rwt, part, total;
+    size_t h, idx, gate, list, rwt, part, total;
 };
 
 FewLayout few_layout(const moe_problem& p) {
@@ -264,6 +264,7 @@ FewLayout few_layout(const moe_problem& p) {
     L.h = take(R * p.d_hidden * 4);   // float32, or two bfloat16 terms
     L.idx = take(R * 4);
     L.gate = take(R * 4);
+    L.list = take(kFewListBytes);
     const bool learned = !(p.flags & MOE_LOGITS_GIVEN), own = few_routes_itself(p.act_dtype, p.d_model, p.n_experts);
     L.rwt = take(learned && !own ? (size_t)p.n_experts * p.d_model * 2 : 0);   // router W^T
     L.part = take(learned && own ? (size_t)p.T * kFewSlices * p.n_experts * 4 : 0);
@@ -1311,8 +1312,8 @@ int32_t moe_forward_few(const moe_problem* p, const void* x, const void* w_route
     return launched(launch_few(p->act_dtype, x, w_router, learned, logits, reinterpret_cast<float*>(at(ws, L.part)), mask,
                                pw + P.w1, pw + P.w2, pw + P.s1, pw + P.s2, y,
                                topk_idx ? topk_idx : reinterpret_cast<int32_t*>(at(ws, L.idx)),
-                               topk_gate ? topk_gate : reinterpret_cast<float*>(at(ws, L.gate)), at(ws, L.h), p->T,
-                               p->d_model, p->n_experts, p->top_k, p->d_hidden, s));
+                               topk_gate ? topk_gate : reinterpret_cast<float*>(at(ws, L.gate)), at(ws, L.list), at(ws, L.h),
+                               p->T, p->d_model, p->n_experts, p->top_k, p->d_hidden, s));
 }
 
 // ----------------------------------------------------------------------------- a few tokens, 4-bit weights

@@ -274,19 +274,37 @@ __device__ __forceinline__ Acts<ACT, NT, TERMS> acts_at(const uint16_t* rows, in
     return o;
 }
 
-// Segment s of both (zero past K: the last segment may be half of one).  rows, K: the weights'; group b is `step(b)`
-// rows from the first.
-template <int ACT, int NB, int NT, int TERMS, typename Step>
-__device__ __forceinline__ void load(const Weights<ACT>& p, const uint8_t* x, const Acts<ACT, NT, TERMS>& in, int s,
-                                     int rows, int K, Step step, WeightPiece<ACT, NB>& w, ActPiece<ACT, NT, TERMS>& o) {
-    const bool inside = (s + 1) * Seg<ACT>::kElems <= K || (threadIdx.x & 63) < 32;
-    const uint32_t term = (uint32_t)K * (ACT == kF32 ? 4u : 2u);
-    if (inside) {
+// Whether a lane's piece of segment s is within K: the last segment may be half of one, the rest of it is zero.
+template <int ACT>
+__device__ __forceinline__ bool inside(int s, int K) {
+    return (s + 1) * Seg<ACT>::kElems <= K || (threadIdx.x & 63) < 32;
+}
+
+// Segment s of the weights.  rows, K: theirs; group b is `step(b)` rows from the first.
+template <int ACT, int NB, typename Step>
+__device__ __forceinline__ void load_weights(const Weights<ACT>& p, int s, int rows, int K, Step step,
+                                             WeightPiece<ACT, NB>& w) {
+    if (inside<ACT>(s, K)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             w.w[b] = load16(p.w + (size_t)step(b) * (K * kWBytes<ACT>) + 256 * (size_t)s, p.wo);
             if (ACT == kMXFP8) w.sc[b] = (p.s + (size_t)(2 * s) * rows * 4 + 4 * step(b))[p.so];
         }
+    } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            w.w[b] = (u32x4){0u, 0u, 0u, 0u};
+            w.sc[b] = 127u;
+        }
+    }
+}
+
+// Segment s of the activations.
+template <int ACT, int NT, int TERMS>
+__device__ __forceinline__ void load_acts(const uint8_t* x, const Acts<ACT, NT, TERMS>& in, int s, int K,
+                                          ActPiece<ACT, NT, TERMS>& o) {
+    const uint32_t term = (uint32_t)K * (ACT == kF32 ? 4u : 2u);
+    if (inside<ACT>(s, K)) {
 #pragma unroll
         for (int g = 0; g < NT; ++g)
 #pragma unroll
@@ -295,11 +313,6 @@ __device__ __forceinline__ void load(const Weights<ACT>& p, const uint8_t* x, co
                 for (int i = 0; i < Seg<ACT>::kX; ++i)
                     o.x[g][t][i] = load16(x + t * (size_t)term + (size_t)(Seg<ACT>::kXBytes * s + 16 * i), in.x[g]);
     } else {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            w.w[b] = (u32x4){0u, 0u, 0u, 0u};
-            w.sc[b] = 127u;
-        }
 #pragma unroll
         for (int g = 0; g < NT; ++g)
 #pragma unroll
@@ -403,6 +416,51 @@ __device__ __forceinline__ int group_rows(const Idx& idx, int R, int E, int g, i
 }
 static_assert(kRows <= 512, "two rows a thread");
 
+// The rows of every expert in use as the down projection takes them: items of up to `most` rows of an expert each, in
+// any order (it does not matter to any sum), rows[item_first ..] those rows.
+struct FewList {
+    int32_t items, pad[3];
+    uint32_t item[kRows];    // expert, first row in rows, rows
+    uint16_t rows[kRows];
+};
+static_assert(sizeof(FewList) == kFewListBytes, "its place in the workspace");
+__device__ __forceinline__ int item_expert(uint32_t it) { return it >> 16; }
+__device__ __forceinline__ int item_first(uint32_t it) { return (it >> 6) & 0x3FF; }
+__device__ __forceinline__ int item_rows(uint32_t it) { return it & 0x3F; }
+
+// A workgroup of 256 writes the list.
+template <typename Idx>
+__device__ __forceinline__ void make_list(const Idx& idx, int R, int E, int most, FewList* list) {
+    __shared__ int32_t s_count[kMaxExperts], s_first[kMaxExperts];
+    __shared__ int32_t s_items, s_total;
+    const int tid = threadIdx.x;
+    for (int e = tid; e < E; e += 256) s_count[e] = 0;
+    if (tid == 0) s_items = s_total = 0;
+    __syncthreads();
+    int mine[2], slot[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = tid + 256 * i;
+        mine[i] = r < R ? idx[r] : -1;
+        slot[i] = mine[i] >= 0 && mine[i] < E ? atomicAdd(&s_count[mine[i]], 1) : -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (slot[i] == 0) {
+            const int n = s_count[mine[i]], first = atomicAdd(&s_total, n), m = (n + most - 1) / most;
+            s_first[mine[i]] = first;
+            const int at = atomicAdd(&s_items, m);
+            for (int j = 0; j < m; ++j)
+                list->item[at + j] = (uint32_t)mine[i] << 16 | (uint32_t)(first + most * j) << 6 | (uint32_t)min(most, n - most * j);
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (slot[i] >= 0) list->rows[s_first[mine[i]] + slot[i]] = (uint16_t)(tid + 256 * i);
+    if (tid == 0) list->items = s_items;
+}
+
 // h of one hidden unit, stored as the down projection reads it.
 template <int ACT>
 __device__ __forceinline__ void store_h(float a, float b, void* h, size_t row, int H, int u) {
@@ -424,19 +482,21 @@ __device__ __forceinline__ void store_h(float a, float b, void* h, size_t row, i
 // Gate and up projections: workgroup = (group, 2 NB hidden units), NB / 2 groups
 // of 4 gate rows and as many up; its waves take the quarters of K, D segments of
 // it requested ahead.  SELECT (T E <= kFused, 256 / (T E) threads for each
-// logit): every workgroup makes the selection for itself, and the first writes
-// it down.
+// logit): every workgroup makes the selection for itself.  One workgroup more,
+// the first, writes down the selection and the down projection's list.
 template <int ACT, int NB, int NT, int D, bool SELECT>
 __global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__ x, int32_t* __restrict__ idx,
                                                      float* __restrict__ gate, const float* __restrict__ part,
                                                      float* __restrict__ logits, const uint8_t* __restrict__ mask,
                                                      const uint8_t* __restrict__ w1, const uint8_t* __restrict__ s1,
-                                                     void* __restrict__ h, int R, int E, int k, int d, int H) {
+                                                     void* __restrict__ h, FewList* __restrict__ list, int R, int E,
+                                                     int k, int d, int H) {
     __shared__ uint16_t s_rows[kRows];
     __shared__ int32_t s_cnt[8];
     __shared__ float red[4][NB][NT][16];
     constexpr int units = 2 * NB;
-    const int nb = H / units, g = blockIdx.x / nb, hb = blockIdx.x - g * nb;
+    const bool lists = blockIdx.x == 0;
+    const int b0 = blockIdx.x - 1, nb = H / units, g = lists ? 0 : b0 / nb, hb = b0 - g * nb;
     int e, n;
     if constexpr (SELECT) {
         __shared__ float s_logit[kFused], s_val[kFused];
@@ -447,7 +507,7 @@ __global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__
             const float v = part ? join_parts(part, tid / E, tid % E, E) : logits[tid];
             s_logit[tid] = v;
             s_rank[tid] = 0;
-            if (part && blockIdx.x == 0) logits[tid] = v;
+            if (part && lists) logits[tid] = v;
         }
         __syncthreads();
         const int parts = 256 / N, at = tid % N, own = at % E, row = at - own;   // 256 / N threads count for each logit
@@ -469,12 +529,20 @@ __global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__
             s_val[t * k + s_rank[tid]] = s_logit[tid];
         }
         __syncthreads();
-        if (blockIdx.x == 0 && tid < R) {
-            idx[tid] = s_idx[tid];
-            gate[tid] = s_idx[tid] < 0 ? 0.f : gate_of(s_val + tid / k * k, k, tid % k);
+        if (lists) {
+            if (tid < R) {
+                idx[tid] = s_idx[tid];
+                gate[tid] = s_idx[tid] < 0 ? 0.f : gate_of(s_val + tid / k * k, k, tid % k);
+            }
+            make_list(s_idx, R, E, 4 * NT, list);
+            return;
         }
         n = group_rows(s_idx, R, E, g, e, s_rows, s_cnt);
     } else {
+        if (lists) {
+            make_list(idx, R, E, 4 * NT, list);
+            return;
+        }
         n = group_rows(idx, R, E, g, e, s_rows, s_cnt);
     }
     if (n == 0) return;
@@ -491,13 +559,19 @@ __global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__
         clear<NB, NT>(acc);
 #pragma unroll
         for (int u = 0; u < D; ++u)
-            if (lo + u < hi) load<ACT, NB, NT, 1>(p, x, in, lo + u, 2 * H, d, step, w[u], a[u]);
+            if (lo + u < hi) {
+                load_weights<ACT, NB>(p, lo + u, 2 * H, d, step, w[u]);
+                load_acts<ACT, NT, 1>(x, in, lo + u, d, a[u]);
+            }
         for (int s = lo; s < hi; s += D) {
 #pragma unroll
             for (int u = 0; u < D; ++u) {
                 if (s + u >= hi) break;
                 multiply<ACT, NB, NT, 1>(w[u], a[u], acc);
-                if (s + u + D < hi) load<ACT, NB, NT, 1>(p, x, in, s + u + D, 2 * H, d, step, w[u], a[u]);
+                if (s + u + D < hi) {
+                    load_weights<ACT, NB>(p, s + u + D, 2 * H, d, step, w[u]);
+                    load_acts<ACT, NT, 1>(x, in, s + u + D, d, a[u]);
+                }
             }
         }
 #pragma unroll
@@ -529,53 +603,26 @@ __global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__
 template <int ACT, int NB, int NT, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __restrict__ h, const int32_t* __restrict__ idx,
                                                               const float* __restrict__ gate,
+                                                              const FewList* __restrict__ list,
                                                               const uint8_t* __restrict__ w2,
                                                               const uint8_t* __restrict__ s2, void* __restrict__ y, int T,
                                                               int E, int k, int d, int H) {
     constexpr int TERMS = ACT == kF32 ? 1 : 2;
     constexpr int cols = 4 * NB, threads = 64 * WAVES;
-    __shared__ int32_t s_count[kMaxExperts], s_first[kMaxExperts];
-    __shared__ uint32_t s_item[kRows];      // expert, first row in s_rows, rows: up to 4 NT rows of an expert
+    __shared__ uint32_t s_item[kRows];
     __shared__ uint16_t s_rows[kRows];
     __shared__ float s_gate[kRows];
     __shared__ uint8_t s_used[kRows];       // whether a slot is in use
-    __shared__ int32_t s_items, s_total;
     extern __shared__ float s_part[];   // [4][T k][cols]
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_index(), R = T * k;
-    // the experts in use and their rows, as items of up to 4 NT rows of an expert; their order does not matter to any sum
-    auto item = [](int e, int first, int n) { return (uint32_t)e << 16 | (uint32_t)first << 6 | (uint32_t)n; };
-    for (int e = tid; e < E; e += threads) s_count[e] = 0;
-    if (tid == 0) s_items = s_total = 0;
-    __syncthreads();
-    constexpr int kMine = (kRows + threads - 1) / threads;
-    int mine[kMine], slot[kMine];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int r = tid + threads * i;
-        mine[i] = r < R ? idx[r] : -1;
-        if (mine[i] < 0 || mine[i] >= E) mine[i] = -1;
-        if (r < R) {
-            s_gate[r] = gate[r];
-            s_used[r] = mine[i] >= 0;
-        }
-        slot[i] = mine[i] >= 0 ? atomicAdd(&s_count[mine[i]], 1) : -1;
+    const int items = uniform(list->items);
+    for (int r = tid; r < R; r += threads) {   // the list's ends are not written: read, not used
+        s_item[r] = list->item[r];
+        s_rows[r] = list->rows[r];
+        s_gate[r] = gate[r];
+        s_used[r] = idx[r] >= 0 && idx[r] < E;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMine; ++i)
-        if (slot[i] == 0) {
-            const int n = s_count[mine[i]], first = atomicAdd(&s_total, n), m = (n + 4 * NT - 1) / (4 * NT);
-            s_first[mine[i]] = first;
-            const int at = atomicAdd(&s_items, m);
-            for (int j = 0; j < m; ++j)
-                s_item[at + j] = item(mine[i], first + 4 * NT * j, min(4 * NT, n - 4 * NT * j));
-        }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMine; ++i)
-        if (slot[i] >= 0) s_rows[s_first[mine[i]] + slot[i]] = (uint16_t)(tid + threads * i);
-    __syncthreads();
-    const int items = uniform(s_items);
     const int c0 = cols * blockIdx.x;
     const int ns = (H + Seg<ACT>::kElems - 1) / Seg<ACT>::kElems, quarter = wave & 3;
     const int lo = quarter * ns / 4, hi = (quarter + 1) * ns / 4;
@@ -589,14 +636,15 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
         auto enter = [&]() {
             if (gi >= items) return;
             const uint32_t it = uniform(s_item[gi]);
-            p = weights_at<ACT>(w2, s2, it >> 16, c0, d, H);
-            in = acts_at<ACT, NT, TERMS>(s_rows + ((it >> 6) & 0x3FF), 0, it & 0x3F, 1, H);
+            p = weights_at<ACT>(w2, s2, item_expert(it), c0, d, H);
+            in = acts_at<ACT, NT, TERMS>(s_rows + item_first(it), 0, item_rows(it), 1, H);
         };
         WeightPiece<ACT, NB> w[D];
         ActPiece<ACT, NT, TERMS> a[D];
         auto request = [&](int u) {
             if (gi >= items) return;
-            load<ACT, NB, NT, TERMS>(p, h, in, si, d, H, step, w[u], a[u]);
+            load_weights<ACT, NB>(p, si, d, H, step, w[u]);
+            load_acts<ACT, NT, TERMS>(h, in, si, H, a[u]);
             if (++si == hi) {
                 si = lo;
                 gi += WAVES / 4;
@@ -616,8 +664,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(const uint8_t* __r
                 request(u);
                 if (++s == hi) {
                     const uint32_t it = uniform(s_item[g]);
-                    const uint16_t* rows = s_rows + ((it >> 6) & 0x3FF);
-                    const int n = it & 0x3F;
+                    const uint16_t* rows = s_rows + item_first(it);
+                    const int n = item_rows(it);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const int r = 4 * t + lane_row();
@@ -663,6 +711,7 @@ struct Choices {
     const uint8_t* mask;
     int32_t* idx;
     float* gate;
+    FewList* list;
 };
 
 template <int ACT, int NT>
@@ -670,21 +719,21 @@ hipError_t launch_products(const void* x_, const Choices& c, const uint8_t* w1, 
                            const uint8_t* s2, void* h_, void* y, int T, int d, int E, int k, int H, hipStream_t s) {
     const int R = T * k, G = std::min(R, E);
     const uint8_t *x = static_cast<const uint8_t*>(x_), *h = static_cast<const uint8_t*>(h_);
-    const dim3 up(G * (H / 8));
+    const dim3 up(1 + G * (H / 8));
     if (c.fused)
         hipLaunchKernelGGL((few_up_kernel<ACT, 4, NT, 1, true>), up, dim3(256), 0, s, x, c.idx, c.gate, c.part, c.logits,
-                           c.mask, w1, s1, h_, R, E, k, d, H);
+                           c.mask, w1, s1, h_, c.list, R, E, k, d, H);
     else
         hipLaunchKernelGGL((few_up_kernel<ACT, 4, NT, 1, false>), up, dim3(256), 0, s, x, c.idx, nullptr, nullptr, nullptr,
-                           nullptr, w1, s1, h_, R, E, k, d, H);
+                           nullptr, w1, s1, h_, c.list, R, E, k, d, H);
     constexpr int D = NT == 1 ? 3 : 2;
     // LDS for the quarters of all rows: 32 KB at most
     if (R <= 256)
         hipLaunchKernelGGL((few_down_kernel<ACT, 2, NT, D, 8>), dim3(d / 8), dim3(512), (size_t)R * 128, s, h, c.idx,
-                           c.gate, w2, s2, y, T, E, k, d, H);
+                           c.gate, c.list, w2, s2, y, T, E, k, d, H);
     else
         hipLaunchKernelGGL((few_down_kernel<ACT, 1, NT, D, 8>), dim3(d / 4), dim3(512), (size_t)R * 64, s, h, c.idx,
-                           c.gate, w2, s2, y, T, E, k, d, H);
+                           c.gate, c.list, w2, s2, y, T, E, k, d, H);
     return hipGetLastError();
 }
 
@@ -712,13 +761,14 @@ bool few_routes_itself(int act, int d, int E) {
 
 hipError_t launch_few(int act, const void* x, const void* w_router, bool learned, float* logits, float* part,
                       const uint8_t* mask, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1, const uint8_t* s2,
-                      void* y, int32_t* idx, float* gate, void* h, int T, int d, int E, int k, int H, hipStream_t s) {
+                      void* y, int32_t* idx, float* gate, void* list, void* h, int T, int d, int E, int k, int H,
+                      hipStream_t s) {
     const u32x4 *xv = static_cast<const u32x4*>(x), *wv = static_cast<const u32x4*>(w_router);
     if (learned && act != kF32)
         hipLaunchKernelGGL(few_logits_kernel<true>, dim3(kFewSlices, T), dim3(256), 0, s, xv, wv, part, E, d);
     else if (learned)
         hipLaunchKernelGGL(few_logits_kernel<false>, dim3(kFewSlices, T), dim3(256), 0, s, xv, wv, part, E, d);
-    const Choices c{T * E <= kFused, learned ? part : nullptr, logits, mask, idx, gate};
+    const Choices c{T * E <= kFused, learned ? part : nullptr, logits, mask, idx, gate, static_cast<FewList*>(list)};
     if (!c.fused)
         hipLaunchKernelGGL(few_select_kernel, dim3(T), dim3(1024), 0, s, c.part, logits, mask, idx, gate, E, k);
     const hipError_t st = hipGetLastError();

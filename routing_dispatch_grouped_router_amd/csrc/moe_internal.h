@@ -16,6 +16,8 @@ constexpr int kMaxTopK = 16;
 constexpr int kDecodeTokens = 256;
 // Most tokens of the block on packed weights for a few tokens (MOE_FEW_MAX_TOKENS).
 constexpr int kFewTokens = 32;
+// Bytes of its list of the experts in use and their rows.
+constexpr size_t kFewListBytes = 16 + kFewTokens * kMaxTopK * 6;
 // Parts of d that its router's products are summed in.
 constexpr int kFewSlices = 16;
 
@@ -296,10 +298,11 @@ hipError_t launch_router_dw(int act, const float* dL, const void* x, float* part
 // Whether launch_few makes the logits of a learned router itself; else they are given (launch_router_logits).
 bool few_routes_itself(int act, int d, int E);
 // The block for T <= kFewTokens: logits (learned) or given ones, selection (mask [T] or NULL), experts.  Scratch: part
-// T kFewSlices E floats (learned), h T k H 4 bytes.
+// T kFewSlices E floats (learned), list kFewListBytes, h T k H 4 bytes.
 hipError_t launch_few(int act, const void* x, const void* w_router, bool learned, float* logits, float* part,
                       const uint8_t* mask, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1, const uint8_t* s2,
-                      void* y, int32_t* idx, float* gate, void* h, int T, int d, int E, int k, int H, hipStream_t s);
+                      void* y, int32_t* idx, float* gate, void* list, void* h, int T, int d, int E, int k, int H,
+                      hipStream_t s);
 
 // ---------------------------------------------------------------- few tokens, 4-bit weights (decode.hip)
 

@@ -738,18 +738,27 @@ hipError_t launch_products(const void* x_, const Choices& c, const uint8_t* w1, 
 }
 
 // Activation rows that a reading of the weights serves: 4 NT.  More of them cost
-// loads and registers whether an expert has them or not (bf16, 16 tokens, d =
-// 2048, E = 8, k = 4, 8 rows an expert on average: 36 us with 8 rows, 38 with 16; 32 tokens,
-// 16 rows: 51 and 48).  Float32 and MXFP8 weights take 8 at most: a second
-// reading comes from the caches and costs less than the registers (MXFP8, 16
-// rows an expert: 39 us with 8, 40 with 16; float32 77 and 84).
+// loads and registers whether an expert has them or not; fewer a second reading,
+// from the caches, where an expert has more.  bf16, d = 2048, rows an expert has on
+// average, us with 8 / 12 / 16 rows a reading:
+//   8 rows: E = 8, H = 1024 34.4 / 36.2 / 38; E = 16, H = 1024 59.3 / 56.6; E = 32, H = 1024 103.9 / 96.9;
+//           E = 8, d = 4096, H = 1536 82.4 / 73.2 (up to 8192 hidden units in all, four workgroups of 8 a compute
+//           unit, all of them run at once with 8 rows' registers and not with 12's)
+//   6 rows: E = 32, H = 1024 89.7 / 92.6;  7 rows: E = 8, H = 4096 98.6 / 97.8
+//   10 rows, 12 / 16: E = 8, H = 4096 103.4 / 109.4, H = 1024 38.9 / 39.3;  12 rows: H = 4096 116.4 / 112.1.
+// Float32 and MXFP8 weights take 8 at most: the second reading costs less than
+// the registers (8 rows an expert, 8 / 12 a reading: MXFP8, E = 8, d = 4096, H =
+// 1536 61.7 / 64.6, 16 rows 89.4 / 93.9 with 16 a reading; float32, E = 32, d = 1024, H = 1024 158 / 168).
 template <int ACT>
 hipError_t launch_products(const void* x, const Choices& c, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1,
                            const uint8_t* s2, void* h, void* y, int T, int d, int E, int k, int H, hipStream_t s) {
     const float rows = (float)T * k / E;   // of an expert, on average
     if (T <= 4 || rows <= 2.f) return launch_products<ACT, 1>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
-    if constexpr (ACT == kBF16)
-        if (T > 8 && rows > 9.f) return launch_products<ACT, 4>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    if constexpr (ACT == kBF16) {
+        if (T > 12 && rows > 11.f) return launch_products<ACT, 4>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+        if (T > 8 && (rows > 9.f || (rows >= 7.f && (long long)E * H > 8192)))
+            return launch_products<ACT, 3>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
+    }
     return launch_products<ACT, 2>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
 }
 

@@ -84,7 +84,8 @@ def _width(n, act):
 SHAPES = [(1, 64, 4, 4, 64), (1, 512, 64, 8, 256), (1, 2048, 8, 2, 1024), (2, 64, 1024, 16, 64), (3, 192, 12, 3, 128),
           (5, 1088, 20, 2, 448), (7, 256, 128, 4, 128), (9, 1024, 64, 8, 512), (13, 128, 99, 5, 192),
           (16, 320, 8, 4, 192), (17, 384, 8, 1, 320), (32, 128, 8, 2, 64), (32, 64, 1, 1, 64), (32, 128, 16, 16, 128),
-          (31, 576, 32, 8, 64), (4, 4096, 16, 2, 128), (3, 128, 512, 4, 64), (2, 8448, 8, 2, 64)]
+          (31, 576, 32, 8, 64), (4, 4096, 16, 2, 128), (3, 128, 512, 4, 64), (2, 8448, 8, 2, 64),
+          (21, 192, 8, 4, 192), (16, 128, 16, 8, 576)]
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "mxfp8"])
@@ -148,7 +149,7 @@ def test_padded_tokens(act, given):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "mxfp8"])
-@pytest.mark.parametrize("T, d, E, k, H", [(32, 512, 8, 4, 256), (20, 384, 64, 6, 128), (9, 320, 12, 2, 64)])
+@pytest.mark.parametrize("T, d, E, k, H", [(32, 512, 8, 4, 256), (20, 384, 64, 6, 128), (9, 320, 12, 2, 64), (21, 256, 8, 4, 1088)])
 def test_a_token_does_not_depend_on_its_batch(T, d, E, k, H, act):
     """Bit for bit the token alone, in a few, and in another order."""
     d, H = _width(d, act), _width(H, act)

@@ -30,8 +30,8 @@
 //
 // The weights' bytes bound it.  d = 4096, E = 64, k = 8, H = 1536, bf16, one token:
 // 61 us (302 MB, 4.9 TB/s; the up projection alone 36 us, 5.6 TB/s, as fast as a
-// kernel that only reads); 16 tokens, d = 2048, E = 8, k = 4, H = 1024: 34 us (101 MB,
-// 3.0 TB/s, of which router and selection 5 us and the launches' starts and ends
+// kernel that only reads); 16 tokens, d = 2048, E = 8, k = 4, H = 1024: 32 us (101 MB,
+// 3.1 TB/s, of which router and selection 5 us and the launches' starts and ends
 // 6); 7 tokens, two of them padding, of 128 MXFP8 experts, k = 4: 39 us (120 MB).  A
 // 2 GiB copy runs at 4.9 TB/s on the same card.
 #include <algorithm>
@@ -485,9 +485,13 @@ __device__ __forceinline__ void store_h(float a, float b, void* h, size_t row, i
 // logit): every workgroup makes the selection for itself.  The first writes
 // down the selection and the down projection's list (a workgroup of its own for
 // that comes before one that no longer fits beside the others: 16 tokens of 8
-// experts 34.5 us instead of 33.7).
+// experts 34.5 us instead of 33.7, before what follows).
+// Four waves a SIMD, so 128 registers, where it would take up to 190: more waves
+// serve better than more loads ahead (bf16, d = 2048, 8 experts, H = 4096: 32 tokens 141
+// -> 134 us, 20 tokens 103 -> 100.5; MXFP8, 64 experts, 32 tokens: 111 -> 104).  Five
+// are slower; with 4 rows a reading it takes 76 to 88, and fewer cost more.
 template <int ACT, int NB, int NT, int D, bool SELECT>
-__global__ __launch_bounds__(256) void few_up_kernel(const uint8_t* __restrict__ x, int32_t* __restrict__ idx,
+__global__ __launch_bounds__(256, NT == 1 ? 1 : 4) void few_up_kernel(const uint8_t* __restrict__ x, int32_t* __restrict__ idx,
                                                      float* __restrict__ gate, const float* __restrict__ part,
                                                      float* __restrict__ logits, const uint8_t* __restrict__ mask,
                                                      const uint8_t* __restrict__ w1, const uint8_t* __restrict__ s1,
@@ -737,16 +741,13 @@ hipError_t launch_products(const void* x_, const Choices& c, const uint8_t* w1, 
 
 // Activation rows that a reading of the weights serves: 4 NT.  More of them cost
 // loads and registers whether an expert has them or not; fewer a second reading,
-// from the caches, where an expert has more.  bf16, d = 2048, rows an expert has on
-// average, us with 8 / 12 / 16 rows a reading:
-//   8 rows: E = 8, H = 1024 34.4 / 36.2 / 38; E = 16, H = 1024 59.3 / 56.6; E = 32, H = 1024 103.9 / 96.9;
-//           E = 8, d = 4096, H = 1536 82.4 / 73.2 (up to 8192 hidden units in all, four workgroups of 8 a compute
-//           unit, all of them run at once with 8 rows' registers and not with 12's)
-//   6 rows: E = 32, H = 1024 89.7 / 92.6;  7 rows: E = 8, H = 4096 98.6 / 97.8
-//   10 rows, 12 / 16: E = 8, H = 4096 103.4 / 109.4, H = 1024 38.9 / 39.3;  12 rows: H = 4096 116.4 / 112.1.
+// from the caches, where an expert has more.  bf16, d = 2048, by the rows that an
+// expert has on average, us with 8 / 12 (/ 16) rows a reading:
+//   5: E = 8, H = 1024 29.5 / 30.8;  6: E = 32, H = 1024 89.4 / 89.1, E = 8, H = 4096 87.4 / 89.7
+//   7: E = 8, H = 1024 32.9 / 31.9;  8: E = 8, H = 1024 33.8 / 32.4, E = 32, H = 1024 103.9 / 93.1
+//   10, 12 / 16: E = 8, H = 4096 100.5 / 106, H = 1024 36.7 / 37.8;  12: H = 4096 115.8 / 108.8, H = 1024 40.0 / 40.5.
 // Float32 and MXFP8 weights take 8 at most: the second reading costs less than
-// the registers (8 rows an expert, 8 / 12 a reading: MXFP8, E = 8, d = 4096, H =
-// 1536 61.7 / 64.6, 16 rows 89.4 / 93.9 with 16 a reading; float32, E = 32, d = 1024, H = 1024 158 / 168).
+// the registers (10 rows an expert: MXFP8, E = 8, H = 4096 83.8 / 85, float32, d = 1024 173 / 181).
 template <int ACT>
 hipError_t launch_products(const void* x, const Choices& c, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1,
                            const uint8_t* s2, void* h, void* y, int T, int d, int E, int k, int H, hipStream_t s) {
@@ -754,7 +755,7 @@ hipError_t launch_products(const void* x, const Choices& c, const uint8_t* w1, c
     if (T <= 4 || rows <= 2.f) return launch_products<ACT, 1>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
     if constexpr (ACT == kBF16) {
         if (T > 12 && rows > 11.f) return launch_products<ACT, 4>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
-        if (T > 8 && (rows > 9.f || (rows >= 7.f && (long long)E * H > 8192)))
+        if (T > 8 && rows >= 7.f)
             return launch_products<ACT, 3>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);
     }
     return launch_products<ACT, 2>(x, c, w1, w2, s1, s2, h, y, T, d, E, k, H, s);

@@ -629,7 +629,9 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  * part of the way to the next code's value and r the low (m) or high (v) 16 bits of
  *   mix(K + i 0x9E3779B9),  K = mix(mix(mix(mix(t) ^ seed) + tensor) ^ block),
  * i the element's place in its block, tensor the place in the list, mix the
- * 32-bit finalizer of MurmurHash3.  Infinite and NaN values have the NaN code.
+ * 32-bit finalizer of MurmurHash3.  The code of a positive sqrt(v) is at least 1,
+ * that is amax / 229376: smaller roots are held that large, and their elements'
+ * steps are smaller for it.  Infinite and NaN values have the NaN code.
  * A MOE_BF16 weight without master: its float32 bits plus the low 16 bits of
  * mix(that number + 0x7F4A7C15), cut to bfloat16.
  *

@@ -64,8 +64,9 @@ def decode8(codes, scales):
     return v * np.repeat(np.asarray(scales, np.float64), BLOCK)[:len(v)]
 
 
-def encode8(x, r16):
-    """(codes, scales, place): place is the code with its fraction, before it is cut."""
+def encode8(x, r16, root=False):
+    """(codes, scales, place): place is the code with its fraction, before it is cut.  root: positive values of blocks
+    that are not zero have a code of 1 at least."""
     n = len(x)
     blocks = -(-n // BLOCK)
     a = np.zeros(blocks * BLOCK)
@@ -77,6 +78,8 @@ def encode8(x, r16):
     lo, hi = E4M3[c], E4M3[c + 1]
     place = c + (a - lo) / (hi - lo) + (r16.astype(np.float64) + 0.5) / 65536
     code = np.minimum(np.floor(place), 126).astype(int)
+    if root:
+        code = np.maximum(code, (x > 0) & np.repeat(amax > 0, BLOCK)[:n])
     code = np.where(np.isfinite(x), code, 127) + np.where(x < 0, 128, 0)
     return code.astype(np.uint8), amax / 448, place
 

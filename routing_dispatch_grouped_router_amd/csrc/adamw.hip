@@ -20,6 +20,12 @@
 // weights without a float32 master, whose last bit is larger than most steps.
 // The random bits are a hash of (seed, step, tensor, block, element): steps are
 // reproducible bit for bit.
+// A positive root has a code of 1 at least.  Both moments' smallest codes are
+// 1/229376 of their block's largest values; a root cut to 0 beside an m that has
+// a code would leave the next step m over little more than eps (blocks whose
+// elements differ by 10^5 and more: steps of 400 to 700 lr, 2.2 with the code).
+// The steps of an element that far below its block's largest are too small
+// instead, as its root is held too large.
 // A root that is right on average has a square too large by the rounding's
 // variance.  A step leaves r close to the code it came from, a part f of the way to
 // the next that is in proportion to 1 - b2, and the variance f (1 - f) with it: v
@@ -157,7 +163,8 @@ __device__ __forceinline__ void decode(u32x2 w, float scale, float (&v)[8]) {
 // h[k].  A value's exponent and fraction as E4M3 has them stand above 20 further
 // bits once it is times 2^-120: 20 random bits (16 and a half) are added there
 // and the sum cut.  Infinite and NaN values get the NaN code and do not count for
-// the scale; a block below 2^-100 is zero.  SIGNED false: no value is below 0.
+// the scale; a block below 2^-100 is zero.  SIGNED false, roots: no value is below
+// 0 (the smallest above it is 2^-75), and a code is 0 only for 0.
 template <bool NT, bool FULL, bool HIGH, bool SIGNED>
 __device__ __forceinline__ void store_codes(uint8_t* p, float* scales, uint64_t i, uint64_t n, const float (&v)[8],
                                             const uint32_t (&h)[8]) {
@@ -183,6 +190,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scales, uint64_t 
         const uint32_t r = HIGH ? (h[k] >> 12) & 0xFFFF0u : (h[k] << 4) & 0xFFFF0u;
         uint32_t c = min((u + (r | 8u)) >> 20, 0x7Eu);
         if (SIGNED) c |= (__float_as_uint(v[k]) >> 24) & 0x80u;
+        else c = max(c, min(__float_as_uint(v[k]), 1u));
         w[k / 4] |= c << (8 * (k % 4));
     }
     if (!finite) {

@@ -68,7 +68,7 @@ struct LayerNormArgs {
     float* mean;         // optional
     float* rstd;         // optional
     int T, chunks;       // 16-byte chunks of a row
-    double inv_d, eps;
+    double d, inv_d, eps;
 };
 
 // TPR threads per row (a wave, or a workgroup of 256); CH chunks per thread
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(LayerNormArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) total += (double)o[i];
     }
-    const double mu = row_sum64<TPR>(total, red[0]) * a.inv_d;
+    const double mu = row_sum64<TPR>(total, red[0]) / a.d;   // a product with a rounded 1 / d misses a value that all share
     double squares = 0.0;
     auto add_squares = [&](const float (&s)[8]) {
 #pragma unroll
@@ -628,7 +628,7 @@ hipError_t launch_layer_norm(int act, const void* x, const void* residual, const
     const LayerNormArgs a{static_cast<const u32x4*>(x), static_cast<const u32x4*>(residual),
                           static_cast<const u32x4*>(weight), static_cast<const u32x4*>(bias),
                           static_cast<u32x4*>(sum), static_cast<u32x4*>(y), static_cast<uint2*>(q),
-                          reinterpret_cast<uint32_t*>(q_scale), mean, rstd, T, d / (bf ? 8 : 4), 1.0 / d, eps};
+                          reinterpret_cast<uint32_t*>(q_scale), mean, rstd, T, d / (bf ? 8 : 4), (double)d, 1.0 / d, eps};
     const bool nt = past_caches((size_t)T * a.chunks * 16);
     if (bf && nt) launch_forward<true, true>(a, s);
     else if (bf) launch_forward<true, false>(a, s);

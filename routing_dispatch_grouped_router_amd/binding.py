@@ -877,7 +877,7 @@ class AdamW(_Params):
         self.m_scale = many("m_scale", m_scale, torch.float32, blocks) if eight else None
         self.r_scale = many("r_scale", r_scale, torch.float32, blocks) if eight else None
         if master is True:
-            master = [w.float() if w.dtype == torch.bfloat16 else None for w in weights]
+            master = [w.detach().float() if w.dtype == torch.bfloat16 else None for w in weights]
         if master is not None:
             master = tuple(master)
             if len(master) != len(weights):

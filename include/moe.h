@@ -714,7 +714,9 @@ int32_t moe_adamw(const moe_param_plan* plan, void* table, const moe_adamw_hyper
  *   topk_idx [T, k], topk_gate [T, k] : out, or NULL (kept in the workspace)
  *   y      : device [T, d] out (activation type, bfloat16 for MOE_MXFP8); may be x
  *   ws     : moe_forward_few_workspace_bytes (host-only query)
- * Ties and gates as moe_route; a token's result does not depend on the other
+ * Ties and gates as moe_route for the same logits; a learned router's are summed in
+ * another order than moe_forward's, so that two that differ by their float32
+ * rounding alone may change places.  A token's result does not depend on the other
  * tokens of the call.  x, w_router, logits, packed_w, y and ws are 16-byte aligned.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T over the limit, T k max(d, H) float32 not
  * below 2^32 bytes), MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_ARG for an

@@ -1,6 +1,8 @@
 // The routed block for a few tokens on the packed weights of moe_pack_weights, for
-// gfx950: from router logits to y in three launches (four where the selection takes
-// one of its own).
+// gfx950: from router logits to y in three launches, four where the selection takes
+// one of its own.  Given logits need no router: two or three.  Expert counts that are
+// no multiple of 8 (float32: 4) have moe_route's router, which for bf16 rows
+// transposes W_r first: up to five.
 //
 //   logits = x W_r, top-k and gates;  h[r] = silu(x[t] Wg) (x[t] Wu) for the
 //   routed rows r = t k + j with expert e_r;  y[t] = sum_j g[t][j] h[t k + j] Wd.
@@ -525,8 +527,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 1 : 4) void few_up_kernel(const uint
                 const uint32_t other = logit_key(s_logit[row + o]);
                 before += other > key || (other == key && o < own);
             }
-            if (parts > 1) atomicAdd(&s_rank[at], before);
-            else s_rank[at] = before;
+            atomicAdd(&s_rank[at], before);
         }
         __syncthreads();
         if (tid < N && s_rank[tid] < k) {
@@ -748,6 +749,12 @@ hipError_t launch_products(const void* x_, const Choices& c, const uint8_t* w1, 
 //   10, 12 / 16: E = 8, H = 4096 100.5 / 106, H = 1024 36.7 / 37.8;  12: H = 4096 115.8 / 108.8, H = 1024 40.0 / 40.5.
 // Float32 and MXFP8 weights take 8 at most: the second reading costs less than
 // the registers (10 rows an expert: MXFP8, E = 8, H = 4096 83.8 / 85, float32, d = 1024 173 / 181).
+// The average counts tokens that are padding, and skewed routing gives one expert several
+// readings in a row.  With Zipf-routed logits (exponent 1.2, the largest expert 16 to 32
+// rows) the choice and the best of the others, us from cold with the launches: 32 tokens, MXFP8,
+// E = 128, k = 4 117 / 118, E = 64, k = 8 135 / 140; bf16, E = 64, k = 8 189 / 193, E = 128, k = 4,
+// H = 512 116 / 112; float32, d = 1024, E = 64, k = 4, H = 512 119 / 115; 16 tokens, bf16,
+// d = 4096, E = 64, k = 8, H = 1536 347 / 329: 5 % off at most.
 template <int ACT>
 hipError_t launch_products(const void* x, const Choices& c, const uint8_t* w1, const uint8_t* w2, const uint8_t* s1,
                            const uint8_t* s2, void* h, void* y, int T, int d, int E, int k, int H, hipStream_t s) {

@@ -626,7 +626,10 @@ int32_t moe_backward_aux(const moe_problem* p, const void* dy, const void* x, co
  * 8-bit moments: a block's scale is amax / 448 (amax over its finite values; 0
  * for a block below 2^-100); a value x has the E4M3 code floor(c + f + (r + 1/2) / 2^16)
  * with its sign, at most 126, for c the code at or below 448 |x| / amax, f the
- * part of the way to the next code's value and r the low (m) or high (v) 16 bits of
+ * part of the way to the next code's value.  The quotients are float32 products
+ * with float32 reciprocals, amax (1 / 448) and |x| (448 (1 / amax)), each rounded,
+ * so that a scale may be a step beside the nearest.  r is the low (m) or high (v)
+ * 16 bits of
  *   mix(K + i 0x9E3779B9),  K = mix(mix(mix(mix(t) ^ seed) + tensor) ^ block),
  * i the element's place in its block, tensor the place in the list, mix the
  * 32-bit finalizer of MurmurHash3.  The code of a positive sqrt(v) is at least 1,

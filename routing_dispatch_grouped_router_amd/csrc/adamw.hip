@@ -181,6 +181,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scales, uint64_t 
     }
     float amax = __uint_as_float(top);
     if (amax < 0x1p-100f) amax = 0.f;
+    // products with rounded reciprocals, as the definition has them (quotients would be another float32 in half of all
+    // blocks, and the step of 50 M elements take 135 us instead of 132)
     if (i % kParamBlock == 0 && (FULL || i < n)) put<float, false>(scales + i / kParamBlock, amax * (1.f / 448.f));
     const float inv = amax > 0.f ? 1.f / amax * 448.f : 0.f;
     u32x2 w = {0u, 0u};

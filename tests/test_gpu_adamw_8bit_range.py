@@ -53,3 +53,25 @@ def test_steps_of_small_elements_stay_bounded(spread):
         after = as_f64(w)
         worst, before = max(worst, np.abs(after - before).max() / lr), after
     assert worst <= 3.5, worst
+
+
+def test_scales_and_codes_are_the_formulas():
+    """With beta1 0 the moment is the gradient.  Its scale is amax (1 / 448) and its place |x| (448 (1 / amax)), every
+    reciprocal and product a float32."""
+    blocks = 4096
+    rng = np.random.default_rng(5)
+    g = (rng.standard_normal((blocks, 128)) * 10 ** rng.uniform(-6, 6, (blocks, 1))).astype(np.float32)
+    op = B.AdamW([torch.zeros(blocks * 128, device=DEV)], [torch.from_numpy(g.reshape(-1)).to(DEV)], lr=0.0, betas=(0.0, 0.95),
+                 weight_decay=0.0, states="8bit", seed=21)
+    op()
+    torch.cuda.synchronize()
+    amax = np.abs(g).max(axis=1)
+    assert np.array_equal(op.m_scale[0].cpu().numpy(), amax * (np.float32(1) / np.float32(448)))
+    a = np.minimum(np.abs(g) * (np.float32(448) * (np.float32(1) / amax))[:, None], np.float32(448)).reshape(-1).astype(np.float64)
+    c = np.minimum(np.searchsorted(Q.E4M3, a, side="right") - 1, 125)
+    r16 = (Q.random_bits(21, 1, 0, a.size) & np.uint32(0xFFFF)).astype(np.float64)
+    place = c + (a - Q.E4M3[c]) / (Q.E4M3[c + 1] - Q.E4M3[c])
+    codes = np.minimum(np.floor(place + (r16 + 0.5) / 65536), 126).astype(int) + np.where(g.reshape(-1) < 0, 128, 0)
+    # float32 has 20 bits below a code's last: a denormal or rounded sum of place and random bits is 2^-20 off at most
+    sure = np.abs((place + (r16 + 0.5) / 65536) - np.round(place + (r16 + 0.5) / 65536)) > 2.0 ** -20
+    assert sure.mean() > 0.99 and np.array_equal(op.m[0].cpu().numpy().astype(int)[sure], codes[sure])

@@ -36,7 +36,8 @@
 // gradient), 28 (float32) or 12 (bf16 alone, 8-bit moments) are read and
 // written once.  50 M elements (three 8 x 2048 x 1024 tensors and small ones):
 // norm 38 us, 5.2 TB/s; step of bf16 with masters 287 us, 5.3 TB/s; with 8-bit
-// moments and no master 131 us, 4.6 TB/s (a 2 GiB copy runs at 4.9 TB/s on the
+// moments and no master 133 us, 4.6 TB/s, passes back to back (launches under a
+// trace, with gaps between them, 289 and 156; a 2 GiB copy runs at 4.9 TB/s on the
 // same card).
 #include <algorithm>
 
@@ -434,7 +435,7 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(unsigned char* table, si
 // 340).  Smaller sets gain from the second: 0.8 M elements 9.3 and 8.4 us with 256
 // and 512; with masters 17 M 95.3 and 86.4, 21 M 120.4 and 118.0, 26 M 153.4 and
 // 155.5; float32 17 M 72.2 and 71.3, 21 M 109.3 and 103.6, 26 M 140.5 and 141.8: 256
-// from 23 M on.  8-bit moments: 2048, past the caches: the arithmetic (300 cycles an element of a wave's 64) needs the waves (131 us;
+// from 23 M on.  8-bit moments: 2048, past the caches: the arithmetic (300 cycles an element of a wave's 64) needs the waves (133 us;
 // 1024 workgroups 134, 512 161, through the caches 137).
 template <int W, bool S8, typename G>
 void launch_kind(const AdamArgs& a, hipStream_t s) {

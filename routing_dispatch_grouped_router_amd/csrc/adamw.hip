@@ -435,8 +435,9 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(unsigned char* table, si
 // 340).  Smaller sets gain from the second: 0.8 M elements 9.3 and 8.4 us with 256
 // and 512; with masters 17 M 95.3 and 86.4, 21 M 120.4 and 118.0, 26 M 153.4 and
 // 155.5; float32 17 M 72.2 and 71.3, 21 M 109.3 and 103.6, 26 M 140.5 and 141.8: 256
-// from 23 M on.  8-bit moments: 2048, past the caches: the arithmetic (300 cycles an element of a wave's 64) needs the waves (133 us;
-// 1024 workgroups 134, 512 161, through the caches 137).
+// from 23 M on.  8-bit moments: 2048, past the caches: the arithmetic (300 cycles
+// an element of a wave's 64) needs the waves (without the roots' least code 131 us,
+// 1024 workgroups 134, 512 161, through the caches 137; with it 133).
 template <int W, bool S8, typename G>
 void launch_kind(const AdamArgs& a, hipStream_t s) {
     const int chunks = a.end - a.first, most = S8 ? 2048 : (chunks >= 11264 ? 256 : 512);
